@@ -19,6 +19,7 @@ import torch
 __all__ = ["spec_verify_greedy", "spec_verify_exact", "spec_verify_relaxed", "spec_verify_tree",
            "spec_verify_power", "spec_sample_drafts", "spec_verify_workspace_bytes", "spec_sample_workspace_bytes",
            "VerifyResult", "TreeResult", "SampleResult", "SpecVerifyError",
+           "spec_token_logprobs", "spec_draft_kl", "spec_linear", "LogprobResult", "SPEC_MAX_TOP",
            "library_path", "load_library", "spec_set_spin_limit", "SPEC_MAX_K", "SPEC_MAX_NODES"]
 
 SPEC_F32, SPEC_BF16 = 0, 1
@@ -89,7 +90,19 @@ def load_library():
     lib.spec_shard_sample_relaxed.argtypes = [P, I, P, Z, P, I, I, I, I, I, P, P, P, P, P, Z, P]
     lib.spec_set_spin_limit.argtypes = [I]
     lib.spec_set_spin_limit.restype = None
+    for fn, n in (("spec_logprobs_workspace_bytes", 4), ("spec_draft_kl_workspace_bytes", 4),
+                  ("spec_linear_workspace_bytes", 4), ("spec_linear_grad_workspace_bytes", 4)):
+        getattr(lib, fn).argtypes = [I] * n
+        getattr(lib, fn).restype = Z
+    lib.spec_token_logprobs.argtypes = [P, I, P, I, I, I, P, P, P, P, P, P, P, Z, P]
+    lib.spec_token_logprobs_grad.argtypes = [P, I, P, P, P, P, I, I, P, P]
+    lib.spec_draft_kl.argtypes = [P, P, I, P, I, I, I, I, P, P, P, Z, P]
+    lib.spec_draft_kl_grad.argtypes = [P, P, I, P, P, P, I, I, I, I, P, P]
+    lib.spec_linear.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P, P, Z, P]
+    lib.spec_linear_grad.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P, P, P, Z, P]
     for fn in ("spec_verify_greedy", "spec_verify_exact", "spec_verify_exact_noalloc",
+               "spec_token_logprobs", "spec_token_logprobs_grad", "spec_draft_kl",
+               "spec_draft_kl_grad", "spec_linear", "spec_linear_grad",
                "spec_verify_relaxed", "spec_verify_tree",
                "spec_verify_power", "spec_sample_drafts", "spec_shard_stats_greedy",
                "spec_shard_stats_tree", "spec_shard_stats_exact", "spec_shard_combine_greedy",
@@ -349,3 +362,7 @@ def spec_verify_tree(target_logits: torch.Tensor, node_tokens: torch.Tensor,
                               _ptr(ws), ws.numel(), _stream_ptr(dev))
     _raise(rc, "spec_verify_tree")
     return TreeResult(path, tok, ln, tlp, blp, st)
+
+
+from .heads import (LogprobResult, SPEC_MAX_TOP, spec_draft_kl, spec_linear,  # noqa: E402
+                    spec_token_logprobs)

@@ -484,6 +484,119 @@ spec_status spec_verify_exact_noalloc(const void *target_logits, const void *dra
                                       float *out_target_logprob, float *out_behavior_logprob,
                                       int32_t *out_status, void *stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Operators on logit rows beside the rules.  Rows, dtype, alignment, streams
+ * and errors as above; a row may hold -inf entries (probability zero) and
+ * values down to the type's lowest, and may hold nothing but -inf.  A row with
+ * a NaN or +inf gives NaN results (alternatives: any tokens of [0, V)).
+ * Limits: rows * (tiles of 16 KiB a row, one more where rows are not 16-byte
+ * aligned) < 2^24.  Sums, maxima and the log-probs are fp32.  Workspaces are
+ * 256-byte aligned and zero-filled before their first use; every call leaves
+ * every byte zero again, so one of the library's workspaces serves these
+ * calls and the rules' in turn on one stream.
+ *
+ * Log probabilities of given tokens, with entropy and top alternatives:
+ * out_logprob[r] = log p_r(tokens[r]) under softmax(row r) and out_entropy[r]
+ * = -sum p ln p, in nats.  The top_n most probable tokens of the row, most
+ * probable first and lowest index first among equals, go to out_top_tokens
+ * with their log-probs; a place past the row's tokens of nonzero probability
+ * gets -1 and -inf.  tokens[r] = -1 marks a padded row, as the rules' outputs
+ * do: its logits are not read and it gets log-prob 0, entropy 0, alternatives
+ * -1 with 0, and a gradient of 0.  A row of -inf alone gives log-prob -inf,
+ * entropy 0 and a gradient of 0.
+ *
+ *   logits            [rows][V] dtype; tokens [rows] int32
+ *   out_logprob, out_entropy [rows] float
+ *   out_top_tokens    [rows][top_n] int32, out_top_logprob [rows][top_n] float
+ *                     (ignored where top_n = 0; top_n <= SPEC_MAX_TOP)
+ *   out_status        [rows] int32: 0, or 1 for a token outside [-1, V): the
+ *                     row is then treated as padded
+ *   out_stats         [rows][4] float, or NULL: what the gradient needs
+ */
+#define SPEC_MAX_TOP 32
+size_t spec_logprobs_workspace_bytes(spec_dtype dtype, int rows, int V, int top_n);
+spec_status spec_token_logprobs(const void *logits, spec_dtype dtype, const int32_t *tokens,
+                                int rows, int V, int top_n, float *out_logprob,
+                                float *out_entropy, int32_t *out_top_tokens,
+                                float *out_top_logprob, int32_t *out_status, float *out_stats,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* The gradient of sum_r grad_logprob[r] logprob[r] + grad_entropy[r]
+ * entropy[r] to the logits, in their dtype: out_grad [rows][V], written
+ * whole.  grad_logprob or grad_entropy may be NULL (zero).  logits, tokens and
+ * stats are the forward call's. */
+spec_status spec_token_logprobs_grad(const void *logits, spec_dtype dtype, const int32_t *tokens,
+                                     const float *stats, const float *grad_logprob,
+                                     const float *grad_entropy, int rows, int V, void *out_grad,
+                                     void *stream);
+
+/*
+ * The divergence of a draft from its target, on the tensors the exact rule
+ * takes: out_kl[b][k] = KL(p || q) in nats, p = softmax(target row k), q =
+ * softmax(draft row k).  target_rows is the target's rows per request, K, or
+ * K + 1 where the bonus row is in place (any number >= K).  Rows with mask 0
+ * are not read and give 0, with a gradient of 0; so does a target row of
+ * -inf alone.  q = 0 where p > 0 gives +inf.
+ *
+ *   target_logits [B][target_rows][V], draft_logits [B][K][V], same dtype
+ *   mask          [B][K] bytes, or NULL (every row counts)
+ *   out_kl        [B][K] float; out_stats [B][K][4] float, or NULL
+ * The gradient is to the draft's logits alone: grad_kl (q - p), in their
+ * dtype; 0 also where the draft's row is -inf alone.
+ */
+size_t spec_draft_kl_workspace_bytes(spec_dtype dtype, int B, int K, int V);
+spec_status spec_draft_kl(const void *target_logits, const void *draft_logits, spec_dtype dtype,
+                          const uint8_t *mask, int B, int K, int target_rows, int V,
+                          float *out_kl, float *out_stats, void *workspace,
+                          size_t workspace_bytes, void *stream);
+spec_status spec_draft_kl_grad(const void *target_logits, const void *draft_logits,
+                               spec_dtype dtype, const uint8_t *mask, const float *stats,
+                               const float *grad_kl, int B, int K, int target_rows, int V,
+                               void *out_grad, void *stream);
+
+/*
+ * The matrix product that a draft head is made of, y = residual + act(x W^T +
+ * bias): a head's residual block, or (no bias, activation or residual) the
+ * output layer that gives the logits the rules read.  Products are summed in
+ * fp32; bias, activation and residual are applied to that sum and y is
+ * rounded once.
+ *
+ *   x [M][K], weight [N][K], bias [N] or NULL   dtype
+ *   residual [M][N] or NULL, out [M][N]         out_dtype
+ *   out_preact [M][N] dtype, or NULL: x W^T + bias, which the gradient of an
+ *                activation needs
+ * dtype SPEC_BF16 takes either out_dtype, SPEC_F32 only SPEC_F32 (else
+ * SPEC_EDTYPE).  Gelu is z Phi(z) with the normal distribution function.
+ * 1 <= M, N, K <= SPEC_MAX_LINEAR, and M * N, M * K and N * K below 2^35.
+ * The workspace needs no initialization and is left with any contents: it is
+ * not one of the zero-filled ones above.
+ */
+#define SPEC_MAX_LINEAR 1048576
+typedef enum {
+    SPEC_ACT_NONE = 0,
+    SPEC_ACT_RELU = 1,
+    SPEC_ACT_GELU = 2,
+    SPEC_ACT_SILU = 3
+} spec_activation;
+size_t spec_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K);
+spec_status spec_linear(const void *x, const void *weight, const void *bias, const void *residual,
+                        spec_dtype dtype, spec_dtype out_dtype, spec_activation activation, int M,
+                        int N, int K, void *out, void *out_preact, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/* Its gradients: with dz = grad_out act'(preact), rounded to dtype, grad_x =
+ * dz W, grad_weight = dz^T x, grad_bias = the sum of dz over rows; the
+ * residual's gradient is grad_out itself.  A NULL output is not computed.
+ * preact may be NULL for SPEC_ACT_NONE; weight is read for grad_x, x for
+ * grad_weight.  grad_out [M][N] out_dtype, the outputs in dtype. */
+size_t spec_linear_grad_workspace_bytes(spec_dtype dtype, int M, int N, int K);
+spec_status spec_linear_grad(const void *x, const void *weight, const void *preact,
+                             const void *grad_out, spec_dtype dtype, spec_dtype out_dtype,
+                             spec_activation activation, int M, int N, int K, void *grad_x,
+                             void *grad_weight, void *grad_bias, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
