@@ -16,6 +16,7 @@
 // exactly in U.
 #include <hip/hip_runtime.h>
 
+#include <limits.h>
 #include <math.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -37,25 +38,28 @@ constexpr int kRsrcWord3 = 0x00020000;  // gfx9-family raw buffer, 32-bit data f
 // A row is read in whole 16-byte blocks whatever its alignment: block i holds
 // the elements i * kVec - shift + j.  The first and the last block may reach
 // past the row, by less than 16 bytes and inside the same aligned block as
-// bytes of the row, and those elements are set to -inf; blocks past the last
+// bytes of the row, and those elements are set to -inf; blocks past the end
 // are not accessed (the descriptor's size ends there).
+__device__ inline float widen(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ inline float widen(float v) { return v; }
+
 template <typename T>
 struct Row {
     static constexpr int kVec = 16 / (int)sizeof(T);
     __amdgpu_buffer_rsrc_t rsrc;
-    int shift, nvec, V;
-    __device__ Row(const T* row, int V_) : V(V_) {
+    int shift, nvec;  // blocks up to the row's end, or to `end`
+    int stop;         // elements up to there
+    __device__ Row(const T* row, int V, int end = INT_MAX) {
         const uintptr_t a = (uintptr_t)row, a0 = a & ~(uintptr_t)15;
         shift = (int)(a - a0) / (int)sizeof(T);
-        nvec = (shift + V + kVec - 1) / kVec;
+        nvec = min((shift + V + kVec - 1) / kVec, end);
+        stop = min(V, nvec * kVec - shift);
         rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a0), (short)0, nvec * 16, kRsrcWord3);
     }
     __device__ int first(int i) const { return i * kVec - shift; }  // element of block i's place 0
     __device__ u32x4 raw(int i) const { return __builtin_amdgcn_raw_buffer_load_b128(rsrc, i * 16, 0, 0); }
-    __device__ void load(int i, float (&v)[kVec]) const {
-        unpack(raw(i), i, v);
-    }
-    __device__ void unpack(u32x4 q, int i, float (&v)[kVec]) const {
+    // the elements e .. e + kVec - 1, widened; -inf outside the row
+    __device__ void unpack(u32x4 q, int e, float (&v)[kVec]) const {
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -66,26 +70,59 @@ struct Row {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(q[j]);
         }
-        const int e = first(i);
-        if (e < 0 || e + kVec > V) {
+        if (e < 0 || e + kVec > stop) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                if (e + j < 0 || e + j >= V) v[j] = -INFINITY;
+                if (e + j < 0 || e + j >= stop) v[j] = -INFINITY;
         }
-    }
-    __device__ static float at(const T* row, int e) {
-        if constexpr (sizeof(T) == 2)
-            return __uint_as_float((uint32_t)row[e] << 16);
-        else
-            return row[e];
     }
 };
 
-__device__ inline uint16_t to_bf16(float f) {  // round to nearest even
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40);
-    return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1)) >> 16);
+// Blocks of one row cut where another row's blocks start: from(i) holds this
+// row's elements that lie under the other row's block i.  Where the two rows
+// are aligned alike that is one load, else two neighbouring ones (the second
+// a cache hit) and a shift by the same count in every lane.
+template <typename T>
+struct Beside {
+    static constexpr int kVec = Row<T>::kVec;
+    Row<T> r;
+    int block, dwords, bytes;  // block offset, then the shift
+    __device__ Beside(const T* row, int V, const Row<T>& other) : r(row, V) {
+        const int d = r.shift - other.shift;
+        block = d < 0 ? -1 : 0;
+        const int by = (d < 0 ? d + kVec : d) * (int)sizeof(T);
+        dwords = by >> 2;
+        bytes = by & 3;
+    }
+    __device__ bool aligned() const { return (dwords | bytes) == 0; }
+    template <bool ALIGNED>
+    __device__ u32x4 from(int i) const {
+        // block -1 lies past the descriptor's size like any other outside block
+        const u32x4 a = r.raw(i + block);
+        if constexpr (ALIGNED) return a;
+        const u32x4 b = r.raw(i + block + 1);
+        u32x4 q;
+        uint32_t x[5];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) {
+            uint32_t w = j < 4 ? a[j & 3] : b[0];
+            if (dwords == 1) w = j + 1 < 4 ? a[(j + 1) & 3] : b[(j + 1) & 3];
+            if (dwords == 2) w = j + 2 < 4 ? a[(j + 2) & 3] : b[(j + 2) & 3];
+            if (dwords == 3) w = j + 3 < 4 ? a[(j + 3) & 3] : b[(j + 3) & 3];
+            x[j] = w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = __builtin_amdgcn_alignbyte(x[j + 1], x[j], bytes);
+        return q;
+    }
+};
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t pack_bf16(float lo, float hi) {  // round to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
+__device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }  // 0 below 2^-126
 
 // A row's gradient, written block by block like Row reads: whole blocks at
 // once where the output row is aligned like the input row.
@@ -93,24 +130,23 @@ template <typename T>
 __device__ inline void store_block(T* row, const Row<T>& r, int i, bool whole, const float (&v)[Row<T>::kVec]) {
     constexpr int kVec = Row<T>::kVec;
     const int e = r.first(i);
-    if (whole && e >= 0 && e + kVec <= r.V) {
-        u32x4 q;
-        if constexpr (sizeof(T) == 2) {
+    u32x4 q;
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                q[j] = (uint32_t)to_bf16(v[2 * j]) | ((uint32_t)to_bf16(v[2 * j + 1]) << 16);
-        } else {
+        for (int j = 0; j < 4; ++j) q[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(v[j]);
-        }
+        for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(v[j]);
+    }
+    if (whole && e >= 0 && e + kVec <= r.stop) {
         *reinterpret_cast<u32x4*>(row + e) = q;
         return;
     }
 #pragma unroll
     for (int j = 0; j < kVec; ++j)
-        if (e + j >= 0 && e + j < r.V) {
+        if (e + j >= 0 && e + j < r.stop) {
             if constexpr (sizeof(T) == 2)
-                row[e + j] = to_bf16(v[j]);
+                row[e + j] = (uint16_t)(q[j >> 1] >> (16 * (j & 1)));
             else
                 row[e + j] = v[j];
         }
@@ -127,7 +163,7 @@ struct Soft {  // of a set of logits: max, sum e^(l-m), sum e^(l-m) (l-m)
 
 // x seen from the larger maximum m of a union
 __device__ inline Soft rebase(const Soft& x, float m) {
-    const float d = x.m - ref_of(m), f = exp2f(d * kLog2e);
+    const float d = x.m - ref_of(m), f = exp2_(d * kLog2e);
     return {m, x.s * f, f > 0.f ? f * fmaf(x.s, d, x.a) : (x.a != x.a ? x.a : 0.f)};
 }
 __device__ inline Soft join(const Soft& x, const Soft& y) {
@@ -140,8 +176,8 @@ struct Pair {  // of two rows' logits: maxima, sums, and U of the comment above
     float m, s, n, r, u;
 };
 __device__ inline Pair rebase(const Pair& x, float m, float n) {
-    const float d = x.m - ref_of(m), f = exp2f(d * kLog2e);
-    const float c = x.n - ref_of(n), g = exp2f(c * kLog2e);
+    const float d = x.m - ref_of(m), f = exp2_(d * kLog2e);
+    const float c = x.n - ref_of(n), g = exp2_(c * kLog2e);
     return {m, x.s * f, n, x.r * g, f > 0.f && x.s != 0.f ? f * fmaf(x.s, d - c, x.u) : 0.f};
 }
 __device__ inline Pair join(const Pair& x, const Pair& y) {
@@ -181,6 +217,9 @@ struct LpArgs {
     float* top_logprob;
     int32_t* status;
     float* stats;  // [rows][4]: max, ln of the sum, entropy, 1 where the row counts
+    int parts, chunk;  // workgroups per row, and blocks each reads
+    uint32_t* counters;
+    uint64_t* records;
 };
 
 // Order of alternatives: by value, then by lowest index; -0 equals +0.
@@ -196,13 +235,150 @@ __device__ inline float key_value(uint64_t k) {
 }
 __device__ inline int key_index(uint64_t k) { return (int)~(uint32_t)k; }
 
+// The n-th largest of the wave's 64 values (n <= 64): the value with fewer
+// than n above it and at least n not below it.  Every lane compares its value
+// with all 64, read back from LDS four at a time.
+__device__ inline float nth_of_wave(float v, int n, float* lds) {
+    const int lane = threadIdx.x & 63;
+    lds[lane] = v;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    int above = 0, from = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float4 o = reinterpret_cast<const float4*>(lds)[j];
+        above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
+        from += (o.x >= v) + (o.y >= v) + (o.z >= v) + (o.w >= v);
+    }
+    const uint64_t at = __ballot(above < n && from >= n);
+    return at ? __shfl(v, __ffsll((unsigned long long)at) - 1) : -INFINITY;
+}
+
+// Best tokens of what a workgroup has read: keys in best[0 .. count), in
+// falling order.
+constexpr int kCand = 1024;
+struct Best {
+    uint64_t key[kCand];
+    uint64_t sorted[SPEC_MAX_TOP];
+    uint64_t red[kWaves];
+    float lane[kWaves][64];
+    float bound[kWaves];
+    int count;
+};
+
+// Keeps the n best of the first c keys, sorted; returns their number.  Keys
+// differ, so a key's place is the number of keys above it.
+__device__ inline int keep_best(Best& b, int c, int n) {
+    const int t = threadIdx.x;
+    for (int i = t; i < c; i += kThreads) {
+        const uint64_t k = b.key[i];
+        int above = 0;
+        for (int j = 0; j < c; ++j) above += b.key[j] > k;
+        if (above < n) b.sorted[above] = k;
+    }
+    __syncthreads();
+    const int m = min(c, n);
+    if (t < m) b.key[t] = b.sorted[t];
+    __syncthreads();
+    return m;
+}
+
+// The same by n rounds of a workgroup-wide maximum over the registers' keys
+// and the first c of the list: for tiles of equal logits, which give more
+// candidates than the list holds.
 template <typename T>
+__device__ int keep_best_by_rounds(Best& b, int c, int n, const float (&v)[kUnroll][Row<T>::kVec], const int (&e)[kUnroll]) {
+    const int t = threadIdx.x;
+    const uint64_t mine = t < c ? b.key[t] : 0;
+    uint64_t last = ~0ull;
+    int got = 0;
+    for (; got < n; ++got) {
+        uint64_t k = mine < last ? mine : 0;
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int j = 0; j < Row<T>::kVec; ++j) {
+                const uint64_t o = key_of(v[u][j], e[u] + j);
+                if (o < last && o > k) k = o;
+            }
+#pragma unroll
+        for (int s = 1; s < 64; s <<= 1) {
+            const uint64_t o = __shfl_xor((unsigned long long)k, s);
+            k = o > k ? o : k;
+        }
+        if ((t & 63) == 0) b.red[t >> 6] = k;
+        __syncthreads();
+        k = b.red[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) k = b.red[w] > k ? b.red[w] : k;
+        if (t == 0) b.sorted[got] = k;
+        __syncthreads();
+        if (k <= kKeyNone) break;
+        last = k;
+    }
+    if (t < got) b.key[t] = b.sorted[t];
+    __syncthreads();
+    return got;
+}
+
+// Outputs of one row from its statistics and its sorted best keys.
+template <typename T>
+__device__ inline void lp_finish(const LpArgs& a, int r, int x, const T* row, const Soft& st, const uint64_t* best, int count) {
+    const int t = threadIdx.x;
+    const bool some = st.s != 0.f;  // false: a row of -inf alone
+    const float ref = ref_of(st.m), ls = logf(st.s), H = some ? ls - st.a / st.s : 0.f;
+    if (t == 0) {
+        a.logprob[r] = some ? (widen(row[x]) - ref) - ls : -INFINITY;
+        a.entropy[r] = H;
+        a.status[r] = 0;
+        if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(ref, ls, H, some ? 1.f : 0.f);
+    }
+    if (t < a.top_n) {
+        const bool is = t < count && best[t] > kKeyNone;
+        a.top_tokens[(size_t)r * a.top_n + t] = is ? key_index(best[t]) : -1;
+        a.top_logprob[(size_t)r * a.top_n + t] = is ? (key_value(best[t]) - ref) - ls : -INFINITY;
+    }
+}
+
+__device__ inline void publish(uint64_t* p, uint64_t v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline uint64_t published(const uint64_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline uint64_t two(float a, float b) { return (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a); }
+__device__ inline float low(uint64_t w) { return __uint_as_float((uint32_t)w); }
+__device__ inline float high(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32)); }
+
+// Whether this workgroup is the last of the row's `parts` to come here: what
+// the others published before is then visible.  The last one leaves the
+// counter at zero.
+__device__ inline bool last_to_come(uint32_t* counter, int parts) {
+    __shared__ int last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t n = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        last = n + 1 == (uint32_t)parts;
+        if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    return last;
+}
+
+// A row is read by `parts` workgroups of `chunk` blocks each; the last of them
+// to finish folds what all have published.  Each keeps running statistics per
+// thread, joined at the end, and (TOP) its best tokens: a bound that at least
+// top_n of the first tile's elements reach, from the threads' maxima, leaves
+// some tens of candidates, which are ranked by counting; later tiles only
+// look for logits above the last one kept (their indices are higher, so a tie
+// loses).
+template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
     constexpr int kVec = Row<T>::kVec;
-    const int r = blockIdx.x, t = threadIdx.x;
+    const int r = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x, w = t >> 6;
     const T* row = static_cast<const T*>(a.logits) + (size_t)r * a.V;
     const int x = a.tokens[r];
     if (x < 0 || x >= a.V) {  // padded, or not a token
+        if (part != 0) return;
         for (int i = t; i < a.top_n; i += kThreads) {
             a.top_tokens[(size_t)r * a.top_n + i] = -1;
             a.top_logprob[(size_t)r * a.top_n + i] = 0.f;
@@ -211,76 +387,133 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
             a.logprob[r] = 0.f;
             a.entropy[r] = 0.f;
             a.status[r] = x != -1;
-            if (a.stats) {
-                float* s = a.stats + (size_t)r * 4;
-                s[0] = s[1] = s[2] = s[3] = 0.f;
-            }
+            if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         return;
     }
-    const Row<T> R(row, a.V);
+    __shared__ Best best;
+    const int begin = part * a.chunk;
+    const Row<T> R(row, a.V, begin + a.chunk);
     Soft st{-INFINITY, 0.f, 0.f};
-    for (int i = t; i < R.nvec; i += kThreads) {
-        float v[kVec];
-        R.load(i, v);
-        float m = v[0];
+    int count = 0;
+    for (int base = begin; base < R.nvec; base += kTileVecs) {
+        u32x4 q[kUnroll];
 #pragma unroll
-        for (int j = 1; j < kVec; ++j) m = fmaxf(m, v[j]);
+        for (int u = 0; u < kUnroll; ++u) q[u] = R.raw(base + u * kThreads + t);
+        float v[kUnroll][kVec], m = -INFINITY;
+        int e[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            e[u] = R.first(base + u * kThreads + t);
+            R.unpack(q[u], e[u], v[u]);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) m = fmaxf(m, v[u][j]);
+        }
         st = rebase(st, fmaxf(st.m, m));
         const float ref = ref_of(st.m);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const float d = v[j] - ref, e = exp2f(d * kLog2e);
-            st.s += e;
-            st.a = fmaf(e, fmaxf(d, -3.0e38f), st.a);
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const float d = v[u][j] - ref, f = exp2_(d * kLog2e);
+                st.s += f;
+                st.a = fmaf(f, fmaxf(d, -3.0e38f), st.a);
+            }
+        if constexpr (TOP) {
+            float bound = -INFINITY;  // logits from it on (first tile) or above it may count
+            const bool first = count < a.top_n;
+            if (first) {
+                const float b = nth_of_wave(m, a.top_n, best.lane[w]);
+                if ((t & 63) == 0) best.bound[w] = b;
+                if (t == 0) best.count = count;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < kWaves; ++i) bound = fmaxf(bound, best.bound[i]);
+            } else {
+                bound = key_value(best.key[a.top_n - 1]);
+                if (t == 0) best.count = count;
+                __syncthreads();
+            }
+            int n = 0;
+            if (first ? m >= bound : m > bound) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) n += v[u][j] > -INFINITY && (first ? v[u][j] >= bound : v[u][j] > bound);
+            }
+            if (n > 0) {
+                int at = atomicAdd(&best.count, n);
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j)
+                        if (v[u][j] > -INFINITY && (first ? v[u][j] >= bound : v[u][j] > bound)) {
+                            if (at < kCand) best.key[at] = key_of(v[u][j], e[u] + j);
+                            ++at;
+                        }
+            }
+            __syncthreads();
+            const int c = best.count;
+            if (c > kCand)
+                count = keep_best_by_rounds<T>(best, count, a.top_n, v, e);
+            else if (c > count)
+                count = keep_best(best, c, a.top_n);
         }
     }
     st = join_group(st);
-    const bool some = st.s != 0.f;  // false: a row of -inf alone
-    const float ref = ref_of(st.m), ls = logf(st.s), H = some ? ls - st.a / st.s : 0.f;
-    if (t == 0) {
-        a.logprob[r] = some ? (Row<T>::at(row, x) - ref) - ls : -INFINITY;
-        a.entropy[r] = H;
-        a.status[r] = 0;
-        if (a.stats) {
-            float* s = a.stats + (size_t)r * 4;
-            s[0] = ref;
-            s[1] = ls;
-            s[2] = H;
-            s[3] = some ? 1.f : 0.f;
-        }
-    }
-    __shared__ uint64_t best[kWaves];
-    uint64_t last = ~0ull;
-    for (int n = 0; n < a.top_n; ++n) {  // the best key below the last one
-        uint64_t k = 0;
-        for (int i = t; i < R.nvec; i += kThreads) {
-            float v[kVec];
-            R.load(i, v);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const uint64_t c = key_of(v[j], R.first(i) + j);
-                if (c < last && c > k) k = c;
-            }
-        }
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) {
-            const uint64_t o = __shfl_xor((unsigned long long)k, s);
-            k = o > k ? o : k;
-        }
-        if ((t & 63) == 0) best[t >> 6] = k;
-        __syncthreads();
-        k = best[0];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) k = best[w] > k ? best[w] : k;
-        __syncthreads();
+    if (a.parts > 1) {
+        const int words = 2 + (TOP ? a.top_n : 0);
+        uint64_t* rec = a.records + ((size_t)r * a.parts + part) * words;
         if (t == 0) {
-            const bool is = k > kKeyNone;
-            a.top_tokens[(size_t)r * a.top_n + n] = is ? key_index(k) : -1;
-            a.top_logprob[(size_t)r * a.top_n + n] = is ? (key_value(k) - ref) - ls : -INFINITY;
+            publish(rec, two(st.m, st.s));
+            publish(rec + 1, two(st.a, 0.f));
         }
-        last = k;
+        if constexpr (TOP)
+            if (t < a.top_n) publish(rec + 2 + t, t < count ? best.key[t] : 0);
+        if (!last_to_come(a.counters + r, a.parts)) return;
+        rec = a.records + (size_t)r * a.parts * words;
+        st = {-INFINITY, 0.f, 0.f};
+        if (t < a.parts) {
+            const uint64_t w0 = published(rec + (size_t)t * words), w1 = published(rec + (size_t)t * words + 1);
+            st = {low(w0), high(w0), low(w1)};
+        }
+        if constexpr (TOP) {
+            // Every part's list is sorted: the n-th largest of the parts' best
+            // (or the largest of their n-th) bounds what can count.
+            const int n = a.top_n, total = a.parts * n;
+            uint64_t bound = 0;
+            if (t < 64) {
+                const uint64_t tail = t < a.parts ? published(rec + (size_t)t * words + 1 + n) : 0;
+                const uint64_t head = t < a.parts ? published(rec + (size_t)t * words + 2) : 0;
+                best.key[t] = head;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                int above = 0;
+                for (int j = 0; j < a.parts; ++j) above += best.key[j] > head;
+                bound = above == n - 1 ? head : 0;
+                bound = tail > bound ? tail : bound;
+#pragma unroll
+                for (int s = 1; s < 64; s <<= 1) {
+                    const uint64_t o = __shfl_xor((unsigned long long)bound, s);
+                    bound = o > bound ? o : bound;
+                }
+                if (t == 0) {
+                    best.red[0] = bound;
+                    best.count = 0;
+                }
+            }
+            __syncthreads();
+            bound = best.red[0];
+            for (int i = t; i < total; i += kThreads) {
+                const uint64_t k = published(rec + (size_t)(i / n) * words + 2 + i % n);
+                if (k != 0 && k >= bound) best.key[atomicAdd(&best.count, 1)] = k;
+            }
+            __syncthreads();
+            count = keep_best(best, best.count, n);
+        }
+        st = join_group(st);
+        for (int i = t; i < a.parts * words; i += kThreads) rec[i] = 0;
     }
+    lp_finish(a, r, x, row, st, best.key, count);
 }
 
 struct LpGradArgs {
@@ -312,10 +545,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
         if (i >= R.nvec) break;
         float v[kVec];
         if (live) {
-            R.load(i, v);
+            R.unpack(R.raw(i), R.first(i), v);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                const float lp = (v[j] - ref) - ls, p = exp2f(lp * kLog2e);
+                const float lp = (v[j] - ref) - ls, p = exp2_(lp * kLog2e);
                 float g = -p * fmaf(ge, fmaxf(lp, -3.0e38f) + H, gl);
                 if (R.first(i) + j == x) g += gl;
                 v[j] = g;
@@ -337,64 +570,117 @@ struct KlArgs {
     float* stats;  // [B*K][4]: max and ln of the sum, target then draft
     const float* g_kl;
     void* grad;
+    int parts, chunk;  // as in LpArgs
+    uint32_t* counters;
+    uint64_t* records;
 };
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
+// Split over workgroups like k_logprobs.  Blocks follow the target's row.
+template <typename T, bool ALIGNED>
+__device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, Pair& st) {
     constexpr int kVec = Row<T>::kVec;
-    const int r = blockIdx.x, t = threadIdx.x;
-    if (a.mask && !a.mask[r]) {
-        if (t == 0) {
-            a.kl[r] = 0.f;
-            if (a.stats) {
-                float* s = a.stats + (size_t)r * 4;
-                s[0] = s[1] = s[2] = s[3] = 0.f;
-            }
+    constexpr int kSteps = kUnroll / 2;  // two rows: as many loads in flight
+    for (int base = begin; base < P.nvec; base += kSteps * kThreads) {
+        u32x4 x[kSteps], y[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int i = base + u * kThreads + (int)threadIdx.x;
+            x[u] = P.raw(i);
+            y[u] = Q.template from<ALIGNED>(i);
         }
-        return;
-    }
-    const int b = r / a.K, k = r % a.K;
-    const Row<T> P(static_cast<const T*>(a.target) + ((size_t)b * a.Kt + k) * a.V, a.V);
-    const T* drow = static_cast<const T*>(a.draft) + (size_t)r * a.V;
-    Pair st{-INFINITY, 0.f, -INFINITY, 0.f, 0.f};
-    // the two rows may be aligned differently: blocks follow the target's, the
-    // draft's elements are read one by one
-    for (int i = t; i < P.nvec; i += kThreads) {
-        float p[kVec], q[kVec];
-        P.load(i, p);
-        const int e = P.first(i);
+        float p[kSteps][kVec], q[kSteps][kVec], m = -INFINITY, n = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            q[j] = e + j >= 0 && e + j < a.V ? Row<T>::at(drow, e + j) : -INFINITY;
-        float m = p[0], n = q[0];
+        for (int u = 0; u < kSteps; ++u) {
+            const int e = P.first(base + u * kThreads + (int)threadIdx.x);
+            P.unpack(x[u], e, p[u]);
+            P.unpack(y[u], e, q[u]);
 #pragma unroll
-        for (int j = 1; j < kVec; ++j) {
-            m = fmaxf(m, p[j]);
-            n = fmaxf(n, q[j]);
+            for (int j = 0; j < kVec; ++j) {
+                m = fmaxf(m, p[u][j]);
+                n = fmaxf(n, q[u][j]);
+            }
         }
         st = rebase(st, fmaxf(st.m, m), fmaxf(st.n, n));
         const float mr = ref_of(st.m), nr = ref_of(st.n);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const float d = p[j] - mr, c = q[j] - nr;
-            const float f = exp2f(d * kLog2e), g = exp2f(c * kLog2e);
-            st.s += f;
-            st.r += g;
-            st.u += f > 0.f ? f * (d - c) : 0.f;
-        }
+        for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const float d = p[u][j] - mr, c = q[u][j] - nr;
+                const float f = exp2_(d * kLog2e), g = exp2_(c * kLog2e);
+                st.s += f;
+                st.r += g;
+                st.u += f > 0.f ? f * (d - c) : 0.f;
+            }
     }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
+    const int r = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x;
+    if (a.mask && !a.mask[r]) {
+        if (t == 0 && part == 0) {
+            a.kl[r] = 0.f;
+            if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        return;
+    }
+    const int b = r / a.K, k = r % a.K, begin = part * a.chunk;
+    const Row<T> P(static_cast<const T*>(a.target) + ((size_t)b * a.Kt + k) * a.V, a.V, begin + a.chunk);
+    const Beside<T> Q(static_cast<const T*>(a.draft) + (size_t)r * a.V, a.V, P);
+    Pair st{-INFINITY, 0.f, -INFINITY, 0.f, 0.f};
+    if (Q.aligned())
+        kl_sweep<T, true>(P, Q, begin, st);
+    else
+        kl_sweep<T, false>(P, Q, begin, st);
     st = join_group(st);
+    if (a.parts > 1) {
+        uint64_t* rec = a.records + ((size_t)r * a.parts + part) * 3;
+        if (t == 0) {
+            publish(rec, two(st.m, st.s));
+            publish(rec + 1, two(st.n, st.r));
+            publish(rec + 2, two(st.u, 0.f));
+        }
+        if (!last_to_come(a.counters + r, a.parts)) return;
+        rec = a.records + (size_t)r * a.parts * 3;
+        st = {-INFINITY, 0.f, -INFINITY, 0.f, 0.f};
+        if (t < a.parts) {
+            const uint64_t w0 = published(rec + t * 3), w1 = published(rec + t * 3 + 1), w2 = published(rec + t * 3 + 2);
+            st = {low(w0), high(w0), low(w1), high(w1), low(w2)};
+        }
+        st = join_group(st);
+        for (int i = t; i < a.parts * 3; i += kThreads) rec[i] = 0;
+    }
     if (t == 0) {
         const float ls = logf(st.s), lr = logf(st.r);
         // an empty target row says nothing; an empty draft row is infinitely far
         a.kl[r] = st.s == 0.f ? 0.f : st.r == 0.f ? INFINITY : st.u / st.s - ls + lr;
-        if (a.stats) {
-            float* s = a.stats + (size_t)r * 4;
-            s[0] = ref_of(st.m);
-            s[1] = ls;
-            s[2] = ref_of(st.n);
-            s[3] = lr;
-        }
+        if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(ref_of(st.m), ls, ref_of(st.n), lr);
+    }
+}
+
+// One workgroup per tile of a draft row: reads both rows, writes the gradient.
+template <typename T, bool ALIGNED>
+__device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Beside<T>& P, T* out, bool whole, int tile, const float4& s, float g) {
+    constexpr int kVec = Row<T>::kVec;
+    u32x4 x[kUnroll], y[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const int i = tile * kTileVecs + u * kThreads + (int)threadIdx.x;
+        x[u] = D.raw(i);
+        y[u] = P.template from<ALIGNED>(i);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const int i = tile * kTileVecs + u * kThreads + (int)threadIdx.x;
+        if (i >= D.nvec) break;
+        float q[kVec], p[kVec];
+        D.unpack(x[u], D.first(i), q);
+        D.unpack(y[u], D.first(i), p);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            q[j] = g * (exp2_(((q[j] - s.z) - s.w) * kLog2e) - exp2_(((p[j] - s.x) - s.y) * kLog2e));
+        store_block(out, D, i, whole, q);
     }
 }
 
@@ -403,35 +689,26 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl_grad(KlArgs a) {
     constexpr int kVec = Row<T>::kVec;
     const int r = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles, t = threadIdx.x;
     const int b = r / a.K, k = r % a.K;
-    const T* prow = static_cast<const T*>(a.target) + ((size_t)b * a.Kt + k) * a.V;
     const T* drow = static_cast<const T*>(a.draft) + (size_t)r * a.V;
     T* out = static_cast<T*>(a.grad) + (size_t)r * a.V;
     const Row<T> D(drow, a.V);
     const bool whole = (((uintptr_t)drow ^ (uintptr_t)out) & 15) == 0;
-    const float* s = a.stats + (size_t)r * 4;
-    const float m = s[0], ls = s[1], n = s[2], lr = s[3];
-    const bool live = (!a.mask || a.mask[r]) && ls != -INFINITY && lr != -INFINITY;
-    const float g = a.g_kl[r];
+    const float4 s = *reinterpret_cast<const float4*>(a.stats + (size_t)r * 4);
+    if ((a.mask && !a.mask[r]) || s.y == -INFINITY || s.w == -INFINITY) {  // nothing to learn from
+        const float zero[kVec] = {};
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const int i = tile * kTileVecs + u * kThreads + t;
-        if (i >= D.nvec) break;
-        float v[kVec];
-        if (live) {
-            D.load(i, v);
-            const int e = D.first(i);
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const float pl = e + j >= 0 && e + j < a.V ? Row<T>::at(prow, e + j) : -INFINITY;
-                const float q = exp2f(((v[j] - n) - lr) * kLog2e), p = exp2f(((pl - m) - ls) * kLog2e);
-                v[j] = g * (q - p);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) v[j] = 0.f;
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = tile * kTileVecs + u * kThreads + t;
+            if (i < D.nvec) store_block(out, D, i, whole, zero);
         }
-        store_block(out, D, i, whole, v);
+        return;
     }
+    const Beside<T> P(static_cast<const T*>(a.target) + ((size_t)b * a.Kt + k) * a.V, a.V, D);
+    const float g = a.g_kl[r];
+    if (P.aligned())
+        kl_grad_tile<T, true>(a, D, P, out, whole, tile, s, g);
+    else
+        kl_grad_tile<T, false>(a, D, P, out, whole, tile, s, g);
 }
 
 // ---------------------------------------------------------------- host side
@@ -447,14 +724,36 @@ inline bool rows_ok(spec_dtype d, long long rows, int V) {
     return rows >= 1 && V >= 1 && V <= SPEC_MAX_V && rows * tiles_of(d, V) < (1ll << 24);
 }
 inline bool ws_ok(const void* p, size_t bytes, size_t need) {
-    return need == 0 || (p && (uintptr_t)p % 256 == 0 && bytes >= need);
+    return p && (uintptr_t)p % 256 == 0 && bytes >= need;
+}
+
+// How a row is split: over as many workgroups as it takes to have kGroups in
+// all, of whole 4 KiB steps.
+constexpr int kGroups = 1024, kMaxParts = 64;
+struct Split {
+    int parts, chunk;
+};
+inline Split split_of(spec_dtype d, long long rows, int V) {
+    const int vec = d == SPEC_BF16 ? 8 : 4;
+    const int nvec = (V + 2 * vec - 2) / vec;  // at the worst alignment
+    const int steps = (nvec + kThreads - 1) / kThreads;
+    const long long want = (kGroups + rows - 1) / rows;
+    int parts = (int)(want < steps ? want : steps);
+    if (parts > kMaxParts) parts = kMaxParts;
+    const int chunk = (steps + parts - 1) / parts * kThreads;
+    return {(nvec + chunk - 1) / chunk, chunk};
+}
+// Counters of the rows, then `words` 8-byte words for each part of each row.
+inline size_t counter_bytes(long long rows) { return ((size_t)rows * 4 + 255) / 256 * 256; }
+inline size_t split_bytes(const Split& s, long long rows, int words) {
+    return s.parts == 1 ? 256 : counter_bytes(rows) + ((size_t)rows * s.parts * words * 8 + 255) / 256 * 256;
 }
 
 }  // namespace
 
 extern "C" size_t spec_logprobs_workspace_bytes(spec_dtype dtype, int rows, int V, int top_n) {
     if (!dtype_ok(dtype) || !rows_ok(dtype, rows, V) || top_n < 0 || top_n > SPEC_MAX_TOP) return 0;
-    return 256;
+    return split_bytes(split_of(dtype, rows, V), rows, 2 + top_n);
 }
 
 extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, const int32_t* tokens, int rows,
@@ -466,12 +765,17 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     if (!logits || !tokens || !out_logprob || !out_entropy || !out_status) return SPEC_EINVAL;
     if (top_n > 0 && (!out_top_tokens || !out_top_logprob)) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_logprobs_workspace_bytes(dtype, rows, V, top_n))) return SPEC_EWORKSPACE;
-    const LpArgs a{logits, tokens, rows, V, top_n, out_logprob, out_entropy, out_top_tokens, out_top_logprob, out_status, out_stats};
+    const Split s = split_of(dtype, rows, V);
+    char* ws = static_cast<char*>(workspace);
+    const LpArgs a{logits, tokens, rows, V, top_n, out_logprob, out_entropy, out_top_tokens, out_top_logprob,
+                   out_status, out_stats, s.parts, s.chunk, reinterpret_cast<uint32_t*>(ws),
+                   reinterpret_cast<uint64_t*>(ws + counter_bytes(rows))};
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    const unsigned grid = (unsigned)rows * (unsigned)s.parts;
     if (dtype == SPEC_BF16)
-        k_logprobs<uint16_t><<<rows, kThreads, 0, st>>>(a);
+        top_n ? k_logprobs<uint16_t, true><<<grid, kThreads, 0, st>>>(a) : k_logprobs<uint16_t, false><<<grid, kThreads, 0, st>>>(a);
     else
-        k_logprobs<float><<<rows, kThreads, 0, st>>>(a);
+        top_n ? k_logprobs<float, true><<<grid, kThreads, 0, st>>>(a) : k_logprobs<float, false><<<grid, kThreads, 0, st>>>(a);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
@@ -499,7 +803,7 @@ inline bool kl_ok(spec_dtype d, int B, int K, int Kt, int V) {
 }  // namespace
 
 extern "C" size_t spec_draft_kl_workspace_bytes(spec_dtype dtype, int B, int K, int V) {
-    return dtype_ok(dtype) && kl_ok(dtype, B, K, K, V) ? 256 : 0;
+    return dtype_ok(dtype) && kl_ok(dtype, B, K, K, V) ? split_bytes(split_of(dtype, (long long)B * K, V), (long long)B * K, 3) : 0;
 }
 
 extern "C" spec_status spec_draft_kl(const void* target_logits, const void* draft_logits, spec_dtype dtype,
@@ -508,12 +812,17 @@ extern "C" spec_status spec_draft_kl(const void* target_logits, const void* draf
     if (!dtype_ok(dtype)) return SPEC_EDTYPE;
     if (!kl_ok(dtype, B, K, target_rows, V) || !target_logits || !draft_logits || !out_kl) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_draft_kl_workspace_bytes(dtype, B, K, V))) return SPEC_EWORKSPACE;
-    const KlArgs a{target_logits, draft_logits, mask, K, target_rows, V, 0, out_kl, out_stats, nullptr, nullptr};
+    const Split s = split_of(dtype, (long long)B * K, V);
+    char* ws = static_cast<char*>(workspace);
+    const KlArgs a{target_logits, draft_logits, mask, K, target_rows, V, 0, out_kl, out_stats, nullptr, nullptr,
+                   s.parts, s.chunk, reinterpret_cast<uint32_t*>(ws),
+                   reinterpret_cast<uint64_t*>(ws + counter_bytes((long long)B * K))};
     const hipStream_t st = static_cast<hipStream_t>(stream);
+    const unsigned grid = (unsigned)(B * K) * (unsigned)s.parts;
     if (dtype == SPEC_BF16)
-        k_draft_kl<uint16_t><<<B * K, kThreads, 0, st>>>(a);
+        k_draft_kl<uint16_t><<<grid, kThreads, 0, st>>>(a);
     else
-        k_draft_kl<float><<<B * K, kThreads, 0, st>>>(a);
+        k_draft_kl<float><<<grid, kThreads, 0, st>>>(a);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
@@ -524,7 +833,7 @@ extern "C" spec_status spec_draft_kl_grad(const void* target_logits, const void*
     if (!kl_ok(dtype, B, K, target_rows, V) || !target_logits || !draft_logits || !stats || !grad_kl || !out_grad)
         return SPEC_EINVAL;
     const int tiles = tiles_of(dtype, V);
-    const KlArgs a{target_logits, draft_logits, mask, K, target_rows, V, tiles, nullptr, const_cast<float*>(stats), grad_kl, out_grad};
+    const KlArgs a{target_logits, draft_logits, mask, K, target_rows, V, tiles, nullptr, const_cast<float*>(stats), grad_kl, out_grad, 1, 0, nullptr, nullptr};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const unsigned grid = (unsigned)(B * K) * (unsigned)tiles;
     if (dtype == SPEC_BF16)
