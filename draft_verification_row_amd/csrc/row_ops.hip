@@ -29,6 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnroll = 4;                       // 16-byte loads per thread and tile
 constexpr int kTileVecs = kThreads * kUnroll;    // 16 KiB
+constexpr int kMaxParts = 64;                     // workgroups per row: one record a lane
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -161,10 +162,12 @@ struct Soft {  // of a set of logits: max, sum e^(l-m), sum e^(l-m) (l-m)
     float m, s, a;
 };
 
-// x seen from the larger maximum m of a union
+// x seen from the larger maximum m of a union (selects, no branches: these
+// sit in the joins' dependent chains)
 __device__ inline Soft rebase(const Soft& x, float m) {
     const float d = x.m - ref_of(m), f = exp2_(d * kLog2e);
-    return {m, x.s * f, f > 0.f ? f * fmaf(x.s, d, x.a) : (x.a != x.a ? x.a : 0.f)};
+    const float a = f * fmaf(x.s, d, x.a);
+    return {m, x.s * f, f > 0.f ? a : 0.f};  // a NaN is in s too
 }
 __device__ inline Soft join(const Soft& x, const Soft& y) {
     const float m = fmaxf(x.m, y.m);
@@ -178,7 +181,8 @@ struct Pair {  // of two rows' logits: maxima, sums, and U of the comment above
 __device__ inline Pair rebase(const Pair& x, float m, float n) {
     const float d = x.m - ref_of(m), f = exp2_(d * kLog2e);
     const float c = x.n - ref_of(n), g = exp2_(c * kLog2e);
-    return {m, x.s * f, n, x.r * g, f > 0.f && x.s != 0.f ? f * fmaf(x.s, d - c, x.u) : 0.f};
+    const float u = f * fmaf(x.s, d - c, x.u);
+    return {m, x.s * f, n, x.r * g, f > 0.f && x.s != 0.f ? u : 0.f};
 }
 __device__ inline Pair join(const Pair& x, const Pair& y) {
     const float m = fmaxf(x.m, y.m), n = fmaxf(x.n, y.n);
@@ -222,58 +226,72 @@ struct LpArgs {
     uint64_t* records;
 };
 
-// Order of alternatives: by value, then by lowest index; -0 equals +0.
-__device__ inline uint64_t key_of(float v, int e) {
-    const uint32_t u = __float_as_uint(v + 0.f);
-    const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return ((uint64_t)o << 32) | (uint32_t)~e;
+__device__ inline uint32_t ordered(float v) {  // whole numbers in the floats' order
+    const uint32_t u = __float_as_uint(v);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-constexpr uint64_t kKeyNone = 0x007fffffffffffffull;  // the largest key of a -inf
-__device__ inline float key_value(uint64_t k) {
-    const uint32_t o = (uint32_t)(k >> 32);
+__device__ inline float unordered(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
+// Order of alternatives: by value, then by lowest index; -0 equals +0.
+__device__ inline uint64_t key_of(float v, int e) { return ((uint64_t)ordered(v + 0.f) << 32) | (uint32_t)~e; }
+constexpr uint64_t kKeyNone = 0x007fffffffffffffull;  // the largest key of a -inf
+__device__ inline float key_value(uint64_t k) { return unordered((uint32_t)(k >> 32)); }
 __device__ inline int key_index(uint64_t k) { return (int)~(uint32_t)k; }
 
-// The n-th largest of the wave's 64 values (n <= 64): the value with fewer
-// than n above it and at least n not below it.  Every lane compares its value
-// with all 64, read back from LDS four at a time.
-__device__ inline float nth_of_wave(float v, int n, float* lds) {
-    const int lane = threadIdx.x & 63;
-    lds[lane] = v;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    int above = 0, from = 0;
+constexpr uint32_t kOrderLowest = 0x00800000u;  // of the lowest finite float
+
+// Two values, as their orders, that at least n and at least k (k <= n <= 64)
+// of the wave's values reach: the n-th and the k-th largest cut to their
+// upper 16 bits (exact for bf16), by bisection with one compare of all lanes
+// a bit.  At least the lowest finite value.
+struct Bounds {
+    uint32_t nth, kth;
+};
+__device__ inline Bounds bounds_of_wave(float v, int n, int k) {
+    const uint32_t o = ordered(v);
+    uint32_t x = 0, y = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const float4 o = reinterpret_cast<const float4*>(lds)[j];
-        above += (o.x > v) + (o.y > v) + (o.z > v) + (o.w > v);
-        from += (o.x >= v) + (o.y >= v) + (o.z >= v) + (o.w >= v);
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t c = x | (1u << bit), d = y | (1u << bit);
+        x = __popcll(__ballot(o >= c)) >= n ? c : x;
+        y = __popcll(__ballot(o >= d)) >= k ? d : y;
     }
-    const uint64_t at = __ballot(above < n && from >= n);
-    return at ? __shfl(v, __ffsll((unsigned long long)at) - 1) : -INFINITY;
+    return {max(x, kOrderLowest), max(y, kOrderLowest)};
 }
 
-// Best tokens of what a workgroup has read: keys in best[0 .. count), in
+// Best tokens of what a workgroup has read: keys in key[0 .. count), in
 // falling order.
-constexpr int kCand = 1024;
+constexpr int kCand = 1024, kFound = 256;
+static_assert(kCand >= SPEC_MAX_TOP * SPEC_MAX_TOP, "the fold's candidates fit");
 struct Best {
     uint64_t key[kCand];
     uint64_t sorted[SPEC_MAX_TOP];
+    uint64_t found[kWaves][kFound];  // of one tile, by wave
     uint64_t red[kWaves];
-    float lane[kWaves][64];
-    float bound[kWaves];
+    Bounds bound[kWaves];
     int count;
 };
 
 // Keeps the n best of the first c keys, sorted; returns their number.  Keys
-// differ, so a key's place is the number of keys above it.
+// differ, so a key's place is the number of keys above it; four neighbouring
+// threads count for one key.
 __device__ inline int keep_best(Best& b, int c, int n) {
-    const int t = threadIdx.x;
-    for (int i = t; i < c; i += kThreads) {
-        const uint64_t k = b.key[i];
+    const int t = threadIdx.x, sub = t & 3;
+    for (int i0 = 0; i0 < c; i0 += kThreads / 4) {
+        const int i = i0 + (t >> 2);
+        const uint64_t k = i < c ? b.key[i] : ~0ull;
         int above = 0;
-        for (int j = 0; j < c; ++j) above += b.key[j] > k;
-        if (above < n) b.sorted[above] = k;
+        for (int j = sub; j < c; j += 16) {
+            uint64_t o[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) o[s] = b.key[min(j + 4 * s, c - 1)];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) above += j + 4 * s < c && o[s] > k;
+        }
+        above += __builtin_amdgcn_mov_dpp(above, 0xB1, 0xf, 0xf, true);  // lane ^ 1
+        above += __builtin_amdgcn_mov_dpp(above, 0x4E, 0xf, 0xf, true);  // lane ^ 2
+        if (sub == 0 && i < c && above < n) b.sorted[above] = k;
     }
     __syncthreads();
     const int m = min(c, n);
@@ -285,8 +303,8 @@ __device__ inline int keep_best(Best& b, int c, int n) {
 // The same by n rounds of a workgroup-wide maximum over the registers' keys
 // and the first c of the list: for tiles of equal logits, which give more
 // candidates than the list holds.
-template <typename T>
-__device__ int keep_best_by_rounds(Best& b, int c, int n, const float (&v)[kUnroll][Row<T>::kVec], const int (&e)[kUnroll]) {
+template <typename T, int U>
+__device__ int keep_best_by_rounds(Best& b, int c, int n, const float (&v)[U][Row<T>::kVec], const int (&e)[U]) {
     const int t = threadIdx.x;
     const uint64_t mine = t < c ? b.key[t] : 0;
     uint64_t last = ~0ull;
@@ -294,7 +312,7 @@ __device__ int keep_best_by_rounds(Best& b, int c, int n, const float (&v)[kUnro
     for (; got < n; ++got) {
         uint64_t k = mine < last ? mine : 0;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < Row<T>::kVec; ++j) {
                 const uint64_t o = key_of(v[u][j], e[u] + j);
@@ -350,28 +368,34 @@ __device__ inline float low(uint64_t w) { return __uint_as_float((uint32_t)w); }
 __device__ inline float high(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32)); }
 
 // Whether this workgroup is the last of the row's `parts` to come here: what
-// the others published before is then visible.  The last one leaves the
-// counter at zero.
+// the others published before is then visible, since published words are
+// written and read with agent-scope atomics, past the XCDs' caches, and have
+// arrived before the counter is raised (a release fence would write back and
+// invalidate the whole XCD's cache: 47 us instead of 17 for the divergence of
+// 160 rows of 128256).  The last one leaves the counter at zero.
 __device__ inline bool last_to_come(uint32_t* counter, int parts) {
     __shared__ int last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
-        const uint32_t n = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t n = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         last = n + 1 == (uint32_t)parts;
         if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
+    asm volatile("" ::: "memory");
     return last;
 }
 
 // A row is read by `parts` workgroups of `chunk` blocks each; the last of them
 // to finish folds what all have published.  Each keeps running statistics per
 // thread, joined at the end, and (TOP) its best tokens: a bound that at least
-// top_n of the first tile's elements reach, from the threads' maxima, leaves
-// some tens of candidates, which are ranked by counting; later tiles only
-// look for logits above the last one kept (their indices are higher, so a tie
-// loses).
-template <typename T, bool TOP>
+// top_n of a tile's elements reach, from the threads' maxima, leaves some tens
+// of candidates, which are ranked by counting; later tiles only look for
+// logits above the last one kept (their indices are higher, so a tie loses).
+// U: blocks per thread and tile.  The next tile is loaded while one is worked
+// on.
+template <typename T, bool TOP, int U>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
     constexpr int kVec = Row<T>::kVec;
     const int r = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x, w = t >> 6;
@@ -396,23 +420,26 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
     const Row<T> R(row, a.V, begin + a.chunk);
     Soft st{-INFINITY, 0.f, 0.f};
     int count = 0;
-    for (int base = begin; base < R.nvec; base += kTileVecs) {
-        u32x4 q[kUnroll];
+    u32x4 q[U];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) q[u] = R.raw(base + u * kThreads + t);
-        float v[kUnroll][kVec], m = -INFINITY;
-        int e[kUnroll];
+    for (int u = 0; u < U; ++u) q[u] = R.raw(begin + u * kThreads + t);
+    for (int base = begin; base < R.nvec; base += U * kThreads) {
+        float v[U][kVec], m = -INFINITY;
+        int e[U];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             e[u] = R.first(base + u * kThreads + t);
             R.unpack(q[u], e[u], v[u]);
+            q[u] = R.raw(base + (U + u) * kThreads + t);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) m = fmaxf(m, v[u][j]);
-        }
         st = rebase(st, fmaxf(st.m, m));
         const float ref = ref_of(st.m);
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float d = v[u][j] - ref, f = exp2_(d * kLog2e);
@@ -420,44 +447,55 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
                 st.a = fmaf(f, fmaxf(d, -3.0e38f), st.a);
             }
         if constexpr (TOP) {
-            float bound = -INFINITY;  // logits from it on (first tile) or above it may count
-            const bool first = count < a.top_n;
-            if (first) {
-                const float b = nth_of_wave(m, a.top_n, best.lane[w]);
-                if ((t & 63) == 0) best.bound[w] = b;
+            uint32_t order;
+            if (count < a.top_n) {
+                // each wave has top_n values from its nth on, and the waves
+                // together from the lowest of their kth on
+                const Bounds o = bounds_of_wave(m, a.top_n, (a.top_n + kWaves - 1) / kWaves);
+                if ((t & 63) == 0) best.bound[w] = o;
                 if (t == 0) best.count = count;
                 __syncthreads();
+                uint32_t nth = 0, kth = ~0u;
 #pragma unroll
-                for (int i = 0; i < kWaves; ++i) bound = fmaxf(bound, best.bound[i]);
+                for (int i = 0; i < kWaves; ++i) {
+                    nth = max(nth, best.bound[i].nth);
+                    kth = min(kth, best.bound[i].kth);
+                }
+                order = max(nth, kth);
             } else {
-                bound = key_value(best.key[a.top_n - 1]);
+                order = ordered(key_value(best.key[a.top_n - 1])) + 1;
                 if (t == 0) best.count = count;
                 __syncthreads();
             }
-            int n = 0;
-            if (first ? m >= bound : m > bound) {
+            const float bound = unordered(order);
+            if (__ballot(m >= bound)) {
+                int n = 0;
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) n += v[u][j] > -INFINITY && (first ? v[u][j] >= bound : v[u][j] > bound);
-            }
-            if (n > 0) {
-                int at = atomicAdd(&best.count, n);
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j)
-                        if (v[u][j] > -INFINITY && (first ? v[u][j] >= bound : v[u][j] > bound)) {
-                            if (at < kCand) best.key[at] = key_of(v[u][j], e[u] + j);
-                            ++at;
+                    for (int j = 0; j < kVec; ++j) {
+                        const bool hit = v[u][j] >= bound;
+                        const uint64_t hits = __ballot(hit);
+                        if (hits) {
+                            const int i = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(hits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
+                            if (hit && i < kFound) best.found[w][i] = key_of(v[u][j], e[u] + j);
+                            n += __popcll(hits);
                         }
+                    }
+                int at = 0;
+                if ((t & 63) == 0) at = atomicAdd(&best.count, n <= kFound ? n : kCand + 1);
+                at = __builtin_amdgcn_readfirstlane(at);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                for (int i = t & 63; i < n && n <= kFound && at + n <= kCand; i += 64) best.key[at + i] = best.found[w][i];
             }
             __syncthreads();
             const int c = best.count;
             if (c > kCand)
-                count = keep_best_by_rounds<T>(best, count, a.top_n, v, e);
+                count = keep_best_by_rounds<T, U>(best, count, a.top_n, v, e);
             else if (c > count)
                 count = keep_best(best, c, a.top_n);
+            else
+                __syncthreads();  // best.count is read before it is set again
         }
     }
     st = join_group(st);
@@ -473,23 +511,31 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
         if (!last_to_come(a.counters + r, a.parts)) return;
         rec = a.records + (size_t)r * a.parts * words;
         st = {-INFINITY, 0.f, 0.f};
-        if (t < a.parts) {
-            const uint64_t w0 = published(rec + (size_t)t * words), w1 = published(rec + (size_t)t * words + 1);
-            st = {low(w0), high(w0), low(w1)};
-        }
         if constexpr (TOP) {
             // Every part's list is sorted: the n-th largest of the parts' best
-            // (or the largest of their n-th) bounds what can count.
+            // (or the largest of their n-th) bounds what can count, and leaves
+            // at most n lists, or fewer parts than n.
+            constexpr int kKeys = kMaxParts * SPEC_MAX_TOP / kThreads;
             const int n = a.top_n, total = a.parts * n;
-            uint64_t bound = 0;
+            uint64_t k[kKeys], head = 0, tail = 0;
+#pragma unroll
+            for (int u = 0; u < kKeys; ++u) {
+                const int i = u * kThreads + t;
+                k[u] = i < total ? published(rec + (size_t)(i / n) * words + 2 + i % n) : 0;
+            }
+            if (t < a.parts) {
+                const uint64_t w0 = published(rec + (size_t)t * words), w1 = published(rec + (size_t)t * words + 1);
+                head = published(rec + (size_t)t * words + 2);
+                tail = published(rec + (size_t)t * words + 1 + n);
+                st = {low(w0), high(w0), low(w1)};
+            }
             if (t < 64) {
-                const uint64_t tail = t < a.parts ? published(rec + (size_t)t * words + 1 + n) : 0;
-                const uint64_t head = t < a.parts ? published(rec + (size_t)t * words + 2) : 0;
                 best.key[t] = head;
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 int above = 0;
-                for (int j = 0; j < a.parts; ++j) above += best.key[j] > head;
-                bound = above == n - 1 ? head : 0;
+#pragma unroll 8
+                for (int j = 0; j < 64; ++j) above += best.key[j] > head;
+                uint64_t bound = above == n - 1 ? head : 0;
                 bound = tail > bound ? tail : bound;
 #pragma unroll
                 for (int s = 1; s < 64; s <<= 1) {
@@ -502,13 +548,15 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
                 }
             }
             __syncthreads();
-            bound = best.red[0];
-            for (int i = t; i < total; i += kThreads) {
-                const uint64_t k = published(rec + (size_t)(i / n) * words + 2 + i % n);
-                if (k != 0 && k >= bound) best.key[atomicAdd(&best.count, 1)] = k;
-            }
+            const uint64_t bound = best.red[0];
+#pragma unroll
+            for (int u = 0; u < kKeys; ++u)
+                if (k[u] != 0 && k[u] >= bound) best.key[atomicAdd(&best.count, 1)] = k[u];
             __syncthreads();
             count = keep_best(best, best.count, n);
+        } else if (t < a.parts) {
+            const uint64_t w0 = published(rec + (size_t)t * words), w1 = published(rec + (size_t)t * words + 1);
+            st = {low(w0), high(w0), low(w1)};
         }
         st = join_group(st);
         for (int i = t; i < a.parts * words; i += kThreads) rec[i] = 0;
@@ -580,26 +628,29 @@ template <typename T, bool ALIGNED>
 __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, Pair& st) {
     constexpr int kVec = Row<T>::kVec;
     constexpr int kSteps = kUnroll / 2;  // two rows: as many loads in flight
-    for (int base = begin; base < P.nvec; base += kSteps * kThreads) {
-        u32x4 x[kSteps], y[kSteps];
+    u32x4 x[kSteps], y[kSteps];
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int i = base + u * kThreads + (int)threadIdx.x;
-            x[u] = P.raw(i);
-            y[u] = Q.template from<ALIGNED>(i);
-        }
+    for (int u = 0; u < kSteps; ++u) {
+        x[u] = P.raw(begin + u * kThreads + (int)threadIdx.x);
+        y[u] = Q.template from<ALIGNED>(begin + u * kThreads + (int)threadIdx.x);
+    }
+    for (int base = begin; base < P.nvec; base += kSteps * kThreads) {
         float p[kSteps][kVec], q[kSteps][kVec], m = -INFINITY, n = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
-            const int e = P.first(base + u * kThreads + (int)threadIdx.x);
+            const int i = base + u * kThreads + (int)threadIdx.x, e = P.first(i);
             P.unpack(x[u], e, p[u]);
             P.unpack(y[u], e, q[u]);
+            x[u] = P.raw(i + kSteps * kThreads);
+            y[u] = Q.template from<ALIGNED>(i + kSteps * kThreads);
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 m = fmaxf(m, p[u][j]);
                 n = fmaxf(n, q[u][j]);
             }
-        }
         st = rebase(st, fmaxf(st.m, m), fmaxf(st.n, n));
         const float mr = ref_of(st.m), nr = ref_of(st.n);
 #pragma unroll
@@ -729,7 +780,7 @@ inline bool ws_ok(const void* p, size_t bytes, size_t need) {
 
 // How a row is split: over as many workgroups as it takes to have kGroups in
 // all, of whole 4 KiB steps.
-constexpr int kGroups = 1024, kMaxParts = 64;
+constexpr int kGroups = 1024;
 struct Split {
     int parts, chunk;
 };
@@ -743,6 +794,16 @@ inline Split split_of(spec_dtype d, long long rows, int V) {
     const int chunk = (steps + parts - 1) / parts * kThreads;
     return {(nvec + chunk - 1) / chunk, chunk};
 }
+// A workgroup that reads one 4 KiB step takes one block a thread.
+template <typename T>
+void launch_logprobs(const LpArgs& a, unsigned grid, hipStream_t st) {
+    const bool one = a.chunk == kThreads;
+    if (a.top_n)
+        one ? k_logprobs<T, true, 1><<<grid, kThreads, 0, st>>>(a) : k_logprobs<T, true, kUnroll><<<grid, kThreads, 0, st>>>(a);
+    else
+        one ? k_logprobs<T, false, 1><<<grid, kThreads, 0, st>>>(a) : k_logprobs<T, false, kUnroll><<<grid, kThreads, 0, st>>>(a);
+}
+
 // Counters of the rows, then `words` 8-byte words for each part of each row.
 inline size_t counter_bytes(long long rows) { return ((size_t)rows * 4 + 255) / 256 * 256; }
 inline size_t split_bytes(const Split& s, long long rows, int words) {
@@ -773,9 +834,9 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const unsigned grid = (unsigned)rows * (unsigned)s.parts;
     if (dtype == SPEC_BF16)
-        top_n ? k_logprobs<uint16_t, true><<<grid, kThreads, 0, st>>>(a) : k_logprobs<uint16_t, false><<<grid, kThreads, 0, st>>>(a);
+        launch_logprobs<uint16_t>(a, grid, st);
     else
-        top_n ? k_logprobs<float, true><<<grid, kThreads, 0, st>>>(a) : k_logprobs<float, false><<<grid, kThreads, 0, st>>>(a);
+        launch_logprobs<float>(a, grid, st);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
