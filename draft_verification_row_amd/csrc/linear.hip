@@ -54,73 +54,331 @@ __device__ inline float act_slope(float z, int act) {
 }
 
 // ------------------------------------------------------------ matrix product
-// C[m][n] = sum_k A[m sam + k sak] B[n sbn + k sbk]
+// out[m][n] = residual + act(sum_k X[m][k] W[n][k] + bias[n]).  Rows of X and W
+// are `ldx` and `ldw` elements apart.
 struct Gemm {
-    const void *A, *B;
-    int64_t sam, sak, sbn, sbk;
+    const void *X, *W;
+    int64_t ldx, ldw;
     int M, N, K;
     const void *bias, *residual;
     int act;
     void *out, *preact;
+    int tiles_n;
 };
 
-constexpr int kTile = 64, kStep = 16;
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 64 x 64 outputs per workgroup, 4 x 4 per thread, fp32 multiply-adds from LDS.
-template <typename T, typename O>
-__global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
-    __shared__ float As[kStep][kTile + 4], Bs[kStep][kTile + 4];
-    const T* A = static_cast<const T*>(g.A);
-    const T* B = static_cast<const T*>(g.B);
-    const int tn = (g.N + kTile - 1) / kTile;
-    const int m0 = (blockIdx.x / tn) * kTile, n0 = (blockIdx.x % tn) * kTile;
-    const int t = threadIdx.x, tx = t % 16, ty = t / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < g.K; k0 += kStep) {
-        for (int i = t; i < kTile * kStep; i += kThreads) {
-            const int k = i % kStep, r = i / kStep;
-            const bool in = k0 + k < g.K;
-            As[k][r] = in && m0 + r < g.M ? to_f(A[(m0 + r) * g.sam + (k0 + k) * g.sak]) : 0.f;
-            Bs[k][r] = in && n0 + r < g.N ? to_f(B[(n0 + r) * g.sbn + (k0 + k) * g.sbk]) : 0.f;
-        }
-        __syncthreads();
+// Both types are staged by 16-byte chunks (8 bf16 or 4 fp32 of one row), and
+// a lane's operand of a matrix instruction is one chunk: 32x32x16 takes two
+// chunks of 32 rows at once, lane l holding row l % 32 and chunk l / 32.  In
+// fp32 the same two chunks are four 32x32x2 products, the i-th of the chunks'
+// i-th elements; the order of the sum over k is the same for both operands.
+__device__ inline f32x16 mfma32(bf16, u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ inline f32x16 mfma32(float, u32x4 a, u32x4 b, f32x16 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
 #pragma unroll
-        for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= g.M || n >= g.N) continue;
-            const size_t at = (size_t)m * g.N + n;
-            float z = acc[i][j];
-            if (g.bias) z += to_f(static_cast<const T*>(g.bias)[n]);
-            if (g.preact) put(static_cast<T*>(g.preact) + at, z);
-            float y = act_of(z, g.act);
-            if (g.residual) y += to_f(static_cast<const O*>(g.residual)[at]);
-            put(static_cast<O*>(g.out) + at, y);
-        }
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[i], y[i], c, 0, 0, 0);
+    return c;
 }
 
-// dz = dy act'(z), rounded to the operands' type
-template <typename T, typename O>
-__global__ __launch_bounds__(kThreads) void k_slope(const O* dy, const T* preact, int act, size_t n, T* dz) {
-    for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kThreads)
-        put(dz + i, to_f(dy[i]) * (preact ? act_slope(to_f(preact[i]), act) : 1.f));
-}
-
-// dbias[n] = sum over m of dz[m][n]: one wave per 64 columns
+// One chunk of a row from element k on: zero past K, which need not be a whole
+// number of chunks, and at any alignment of the row.
 template <typename T>
-__global__ __launch_bounds__(64) void k_colsum(const T* dz, int M, int N, T* out) {
-    const int n = blockIdx.x * 64 + threadIdx.x;
-    if (n >= N) return;
+__device__ inline u32x4 chunk_of(const T* row, int k, int K) {
+    constexpr int kElems = 16 / (int)sizeof(T);
+    struct Any {
+        u32x4 v;
+    } __attribute__((packed, aligned(sizeof(T))));
+    if (k + kElems <= K) return reinterpret_cast<const Any*>(row + k)->v;
+    u32x4 q = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < kElems; ++j)
+        if (k + j < K) {
+            if constexpr (sizeof(T) == 2)
+                q[j >> 1] |= (uint32_t)row[k + j] << (16 * (j & 1));
+            else
+                q[j] = __float_as_uint(row[k + j]);
+        }
+    return q;
+}
+
+// ------------------------------------------------------------------ epilogue
+__device__ inline uint32_t pack_bf16(float lo, float hi) {  // round to nearest even
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
+}
+__device__ inline void put4(float* p, const float (&v)[4]) { *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]}; }
+__device__ inline void put4(bf16* p, const float (&v)[4]) {
+    *reinterpret_cast<u32x2*>(p) = (u32x2){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+__device__ inline void get4(const float* p, float (&v)[4]) {
+    const f32x4 q = *reinterpret_cast<const f32x4*>(p);
+    for (int i = 0; i < 4; ++i) v[i] = q[i];
+}
+__device__ inline void get4(const bf16* p, float (&v)[4]) {
+    const u32x2 q = *reinterpret_cast<const u32x2*>(p);
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float((i & 1) ? q[i >> 1] & 0xffff0000u : q[i >> 1] << 16);
+}
+
+// Four neighbouring outputs of row m from n on (n % 4 == 0).  whole: N is a
+// multiple of 4 and every array aligned to four elements.
+template <typename T, typename O>
+__device__ inline void finish4(const Gemm& g, int m, int n, bool whole, float (&z)[4]) {
+    const size_t at = (size_t)m * g.N + n;
+    const T* bias = static_cast<const T*>(g.bias);
+    T* pre = static_cast<T*>(g.preact);
+    const O* res = static_cast<const O*>(g.residual);
+    O* out = static_cast<O*>(g.out);
+    if (whole) {
+        float v[4];
+        if (bias) {
+            get4(bias + n, v);
+            for (int i = 0; i < 4; ++i) z[i] += v[i];
+        }
+        if (pre) put4(pre + at, z);
+        for (int i = 0; i < 4; ++i) z[i] = act_of(z[i], g.act);
+        if (res) {
+            get4(res + at, v);
+            for (int i = 0; i < 4; ++i) z[i] += v[i];
+        }
+        put4(out + at, z);
+        return;
+    }
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= g.N) break;
+        float v = z[i];
+        if (bias) v += to_f(bias[n + i]);
+        if (pre) put(pre + at + i, v);
+        v = act_of(v, g.act);
+        if (res) v += to_f(res[at + i]);
+        put(out + at + i, v);
+    }
+}
+template <typename T, typename O>
+__device__ inline bool four_at_once(const Gemm& g) {
+    const uintptr_t t = (uintptr_t)g.bias | (uintptr_t)g.preact, o = (uintptr_t)g.residual | (uintptr_t)g.out;
+    return g.N % 4 == 0 && t % (4 * sizeof(T)) == 0 && o % (4 * sizeof(O)) == 0;
+}
+
+// -------------------------------------------------------------- tiled product
+// BM x BN outputs per workgroup of four waves, two by two; a wave has
+// (BM/2) x (BN/2) in 32 x 32 blocks, weights as the instruction's first
+// operand, so that a lane ends with four neighbouring n of one m.  The rows'
+// next 128 bytes (64 bf16, 32 fp32) are one stage in LDS: chunk c of row r lies
+// at place c ^ (r & 7) of its row, which spreads the 32 rows a wave reads
+// at one chunk over all banks.
+constexpr int kRowBytes = 128, kRowChunks = kRowBytes / 16;
+
+// Consecutive workgroups go to different XCDs (blockIdx % 8); each XCD takes a
+// run of neighbouring tiles instead, in columns of kGroupM tiles along m, so
+// that its L2 holds what its tiles share.
+constexpr int kXcds = 8, kGroupM = 8;
+__device__ inline void tile_of(int id, int count, int tiles_m, int tiles_n, int& tm, int& tn) {
+    const int per = count / kXcds, rest = count % kXcds, x = id % kXcds, i = id / kXcds;
+    const int at = x * per + min(x, rest) + i;
+    const int group = kGroupM * tiles_n, first = at / group * kGroupM;
+    const int high = min(kGroupM, tiles_m - first), in = at % group;
+    tm = first + in % high;
+    tn = in / high;
+}
+
+// 16 bytes a lane from the buffer straight to LDS at base + lane * 16.
+__device__ inline void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, uint32_t voffset, uint32_t soffset) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(voffset), "s"(rsrc), "s"(soffset) : "memory");
+}
+
+template <typename T, typename O, int BM, int BN, int STAGES, bool DIRECT>
+__global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
+    constexpr int kElems = 16 / (int)sizeof(T), kStep = kElems * kRowChunks;
+    constexpr int FM = BM / 64, FN = BN / 64;       // 32 x 32 blocks a wave
+    constexpr int kRows = BM + BN;                  // rows of a stage: W's, then X's
+    constexpr int kLoads = kRows / 8 / 4;           // 1 KiB loads a wave and stage
+    constexpr int kStageBytes = kRows * kRowBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[STAGES][kStageBytes];
+    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    int tm, tn;
+    const int tiles_m = (g.M + BM - 1) / BM;
+    tile_of(blockIdx.x, gridDim.x, tiles_m, g.tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const T* W = static_cast<const T*>(g.W) + (int64_t)n0 * g.ldw;
+    const T* X = static_cast<const T*>(g.X) + (int64_t)m0 * g.ldx;
+
+    // load i of this wave: eight rows, lane / 8 the row and lane % 8 the place
+    const int r8 = lane >> 3, c8 = (lane & 7) ^ r8;  // rows start at multiples of 8
+    auto row_of = [&](int i) { return (i * 4 + w) * 8; };
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(W), (short)0, 0x7fffffff, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(X), (short)0, 0x7fffffff, 0x00020000);
+    uint32_t off[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        // rows past the matrix read its last row; their products are dropped
+        const int r = row_of(i) + r8;
+        const int64_t e = row_of(i) < BN ? min(r, g.N - 1 - n0) * g.ldw : min(r - BN, g.M - 1 - m0) * g.ldx;
+        off[i] = (uint32_t)(e * (int64_t)sizeof(T)) + (uint32_t)c8 * 16;
+    }
+    auto load_direct = [&](int stage, int step) {
+        const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&lds[stage][0];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = row_of(i);
+            to_lds(i * 32 < BN ? rw : rx, base + r * kRowBytes, off[i], (uint32_t)step * kRowBytes);
+        }
+    };
+    auto fetch = [&](int step, u32x4 (&q)[kLoads]) {  // the same through registers, any alignment
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = row_of(i) + r8;
+            const T* row = row_of(i) < BN ? W + min(r, g.N - 1 - n0) * g.ldw : X + min(r - BN, g.M - 1 - m0) * g.ldx;
+            q[i] = chunk_of(row, step * kStep + c8 * kElems, g.K);
+        }
+    };
+    auto place = [&](int stage, const u32x4 (&q)[kLoads]) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            *reinterpret_cast<u32x4*>(&lds[stage][row_of(i) * kRowBytes + lane * 16]) = q[i];
+    };
+
+    f32x16 acc[FN][FM] = {};
+    const int wn = (w & 1) * (BN / 2), wm = (w >> 1) * (BM / 2), l = lane & 31, h = lane >> 5;
+    auto compute = [&](int stage) {
+        const char* s = &lds[stage][0];
+#pragma unroll
+        for (int k = 0; k < kRowChunks / 2; ++k) {
+            u32x4 a[FN], b[FM];
+            const int place_at = ((2 * k + h) ^ (l & 7)) * 16;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+                a[i] = *reinterpret_cast<const u32x4*>(s + (wn + i * 32 + l) * kRowBytes + place_at);
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                b[i] = *reinterpret_cast<const u32x4*>(s + (BN + wm + i * 32 + l) * kRowBytes + place_at);
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] = mfma32(T(), a[i], b[j], acc[i][j]);
+        }
+    };
+
+    const int steps = (g.K + kStep - 1) / kStep, full = DIRECT ? g.K / kStep : 0;
+    if constexpr (DIRECT) {
+        // STAGES - 1 steps are on their way while one is worked on
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s)
+            if (s < full) load_direct(s, s);
+        for (int s = 0; s < full; ++s) {
+            if (s + STAGES - 1 <= full)
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(kLoads * (STAGES - 2)) : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            // every wave's part of stage s has arrived, and no wave still
+            // reads the stage that is loaded next
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (s + STAGES - 1 < full) load_direct((s + STAGES - 1) % STAGES, s + STAGES - 1);
+            compute(s % STAGES);
+        }
+    }
+    for (int s = full; s < steps; ++s) {
+        u32x4 q[kLoads];
+        fetch(s, q);
+        __syncthreads();
+        place(s % STAGES, q);
+        __syncthreads();
+        compute(s % STAGES);
+    }
+
+    // Each wave turns its blocks, 32 rows of m at a time, through its own part
+    // of the LDS, so that neighbouring lanes have neighbouring n.
+    constexpr int kCols = BN / 2, kPitch = kCols + 4;
+    static_assert(4 * 32 * kPitch * 4 <= STAGES * kStageBytes, "the epilogue's tiles fit");
+    __syncthreads();
+    float* turn = reinterpret_cast<float*>(&lds[0][0]) + w * 32 * kPitch;
+    const bool whole = four_at_once<T, O>(g);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(turn + l * kPitch + i * 32 + q * 8 + h * 4) =
+                    (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        constexpr int kLanes = kCols / 4, kAtOnce = 64 / kLanes;
+        const int n = n0 + wn + lane % kLanes * 4;
+        for (int r = lane / kLanes; r < 32; r += kAtOnce) {
+            const int m = m0 + wm + j * 32 + r;
+            const f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * kPitch + lane % kLanes * 4);
+            float z[4] = {v[0], v[1], v[2], v[3]};
+            if (m < g.M && n < g.N) finish4<T, O>(g, m, n, whole, z);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// ---------------------------------------------------------- gradients' inputs
+// dz = dy act'(z) to dz [M][ld] and, turned, to dzt [N][ldt], rounded, zero up
+// to the rows' ends; sums of 64 rows' unrounded dz to part [M/64][N].  Each of
+// the three is optional.  The same kernel turns a matrix (dy alone).
+struct Slope {
+    const void *dy, *preact;
+    int act, M, N;
+    void *dz, *dzt;
+    int64_t ld, ldt;
+    float* part;
+};
+
+template <typename I, typename T>
+__global__ __launch_bounds__(kThreads) void k_slope(Slope a) {
+    __shared__ float tile[64][65];
+    const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64, t = threadIdx.x, c = t & 63, r0 = t >> 6;
+    float sum = 0.f;
+    for (int r = r0; r < 64; r += 4) {
+        const int m = m0 + r, n = n0 + c;
+        float v = 0.f;
+        if (m < a.M && n < a.N) {
+            const size_t at = (size_t)m * a.N + n;
+            v = to_f(static_cast<const I*>(a.dy)[at]);
+            if (a.preact) v *= act_slope(to_f(static_cast<const T*>(a.preact)[at]), a.act);
+        }
+        sum += v;
+        tile[r][c] = v;
+        if (a.dz && m < a.M && n < a.ld) put(static_cast<T*>(a.dz) + (size_t)m * a.ld + n, v);
+    }
+    __syncthreads();
+    if (a.dzt)
+        for (int r = r0; r < 64; r += 4) {
+            const int n = n0 + r, m = m0 + c;
+            if (n < a.N && m < a.ldt) put(static_cast<T*>(a.dzt) + (size_t)n * a.ldt + m, tile[c][r]);
+        }
+    if (a.part) {
+        __shared__ float sums[4][64];
+        sums[r0][c] = sum;
+        __syncthreads();
+        if (r0 == 0 && n0 + c < a.N)
+            a.part[(size_t)blockIdx.y * a.N + n0 + c] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+    }
+}
+
+// dbias[n] = the sum of the parts, in a fixed order: 64 columns a workgroup,
+// every fourth part to a wave
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_bias_sum(const float* part, int parts, int N, T* out) {
+    __shared__ float sums[4][64];
+    const int c = threadIdx.x & 63, w = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
     float s = 0.f;
-    for (int m = 0; m < M; ++m) s += to_f(dz[(size_t)m * N + n]);
-    put(out + n, s);
+    if (n < N)
+        for (int p = w; p < parts; p += 4) s += part[(size_t)p * N + n];
+    sums[w][c] = s;
+    __syncthreads();
+    if (w == 0 && n < N) put(out + n, (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]));
 }
 
 // ---------------------------------------------------------------- host side
@@ -139,14 +397,63 @@ inline bool ws_ok(const void* p, size_t bytes, size_t need) {
 }
 inline spec_status launched() { return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP; }
 
-void launch_gemm(const Gemm& g, spec_dtype d, spec_dtype o, hipStream_t st) {
-    const unsigned grid = (unsigned)((g.M + kTile - 1) / kTile) * (unsigned)((g.N + kTile - 1) / kTile);
-    if (d == SPEC_F32)
-        k_gemm<float, float><<<grid, kThreads, 0, st>>>(g);
-    else if (o == SPEC_F32)
-        k_gemm<bf16, float><<<grid, kThreads, 0, st>>>(g);
+template <typename T, typename O, int B, int STAGES, bool DIRECT>
+void launch_tiles(Gemm g, hipStream_t st) {
+    const int tm = (g.M + B - 1) / B;
+    g.tiles_n = (g.N + B - 1) / B;
+    k_gemm<T, O, B, B, STAGES, DIRECT><<<(unsigned)tm * (unsigned)g.tiles_n, kThreads, 0, st>>>(g);
+}
+template <typename T, typename O>
+void launch_typed(const Gemm& g, hipStream_t st) {
+    const uintptr_t a = (uintptr_t)g.X | (uintptr_t)g.W | (uintptr_t)(g.ldx * (int64_t)sizeof(T)) | (uintptr_t)(g.ldw * (int64_t)sizeof(T));
+    auto tiles = [&](int b) { return (long long)((g.M + b - 1) / b) * ((g.N + b - 1) / b); };
+    if (a % 16 != 0)
+        launch_tiles<T, O, 64, 2, false>(g, st);
+    else if (tiles(256) >= 200)
+        launch_tiles<T, O, 256, 2, true>(g, st);
+    else if (tiles(128) >= 200)
+        launch_tiles<T, O, 128, 4, true>(g, st);
     else
-        k_gemm<bf16, bf16><<<grid, kThreads, 0, st>>>(g);
+        launch_tiles<T, O, 64, 4, true>(g, st);
+}
+void launch_gemm(const Gemm& g, spec_dtype d, spec_dtype o, hipStream_t st) {
+    if (d == SPEC_F32)
+        launch_typed<float, float>(g, st);
+    else if (o == SPEC_F32)
+        launch_typed<bf16, float>(g, st);
+    else
+        launch_typed<bf16, bf16>(g, st);
+}
+
+// The gradients' workspace: dz, dz turned, x and W turned, rows padded to whole
+// chunks, and the bias gradient's parts.
+struct GradLayout {
+    int64_t np, mp;  // padded N and M
+    size_t dz, dzt, xt, wt, part, total;
+};
+inline GradLayout grad_layout(spec_dtype d, long long M, long long N, long long K) {
+    const long long e = (long long)elem(d), c = 16 / e;
+    GradLayout l;
+    l.np = (N + c - 1) / c * c;
+    l.mp = (M + c - 1) / c * c;
+    l.dz = 0;
+    l.dzt = align_up(l.dz + (size_t)(M * l.np * e), 256);
+    l.xt = align_up(l.dzt + (size_t)(N * l.mp * e), 256);
+    l.wt = align_up(l.xt + (size_t)(K * l.mp * e), 256);
+    l.part = align_up(l.wt + (size_t)(K * l.np * e), 256);
+    l.total = align_up(l.part + (size_t)((M + 63) / 64 * N * 4), 256);
+    return l;
+}
+
+void launch_slope(const Slope& a, spec_dtype in, spec_dtype d, hipStream_t st) {
+    // the turned rows' padding lies under the last blocks too
+    const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
+    if (d == SPEC_F32)
+        k_slope<float, float><<<grid, kThreads, 0, st>>>(a);
+    else if (in == SPEC_F32)
+        k_slope<float, bf16><<<grid, kThreads, 0, st>>>(a);
+    else
+        k_slope<bf16, bf16><<<grid, kThreads, 0, st>>>(a);
 }
 
 }  // namespace
@@ -163,14 +470,14 @@ extern "C" spec_status spec_linear(const void* x, const void* weight, const void
     if (!types_ok(dtype, out_dtype)) return SPEC_EDTYPE;
     if (!sizes_ok(M, N, K) || !act_ok(activation) || !x || !weight || !out) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_linear_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
-    const Gemm g{x, weight, K, 1, K, 1, M, N, K, bias, residual, activation, out, out_preact};
+    const Gemm g{x, weight, K, K, M, N, K, bias, residual, activation, out, out_preact, 0};
     launch_gemm(g, dtype, out_dtype, static_cast<hipStream_t>(stream));
     return launched();
 }
 
 extern "C" size_t spec_linear_grad_workspace_bytes(spec_dtype dtype, int M, int N, int K) {
     if (!types_ok(dtype, SPEC_F32) || !sizes_ok(M, N, K)) return 0;
-    return align_up((size_t)M * N * elem(dtype), 256);
+    return grad_layout(dtype, M, N, K).total;
 }
 
 extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const void* preact, const void* grad_out,
@@ -183,24 +490,33 @@ extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const
     if ((grad_x && !weight) || (grad_weight && !x)) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_linear_grad_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const size_t n = (size_t)M * N;
-    const unsigned grid = (unsigned)((n + kThreads - 1) / kThreads < 65536 ? (n + kThreads - 1) / kThreads : 65536);
+    const GradLayout lay = grad_layout(dtype, M, N, K);
+    char* ws = static_cast<char*>(workspace);
     const void* z = activation == SPEC_ACT_NONE ? nullptr : preact;
-    if (dtype == SPEC_F32)
-        k_slope<float, float><<<grid, kThreads, 0, st>>>((const float*)grad_out, (const float*)z, activation, n, (float*)workspace);
-    else if (out_dtype == SPEC_F32)
-        k_slope<bf16, float><<<grid, kThreads, 0, st>>>((const float*)grad_out, (const bf16*)z, activation, n, (bf16*)workspace);
-    else
-        k_slope<bf16, bf16><<<grid, kThreads, 0, st>>>((const bf16*)grad_out, (const bf16*)z, activation, n, (bf16*)workspace);
+    // without an activation dy is dz where it has the operands' type and
+    // aligned rows
+    const bool as_is = !z && dtype == out_dtype && lay.np == N && (uintptr_t)grad_out % 16 == 0;
+    const Slope s{grad_out, z, activation, M, N, grad_x && !as_is ? ws + lay.dz : nullptr,
+                  grad_weight ? ws + lay.dzt : nullptr, lay.np, lay.mp,
+                  grad_bias ? reinterpret_cast<float*>(ws + lay.part) : nullptr};
+    if (s.dz || s.dzt || s.part) launch_slope(s, out_dtype, dtype, st);
     if (grad_bias) {
+        const float* part = reinterpret_cast<const float*>(ws + lay.part);
+        const int parts = (M + 63) / 64;
         if (dtype == SPEC_F32)
-            k_colsum<float><<<(N + 63) / 64, 64, 0, st>>>((const float*)workspace, M, N, (float*)grad_bias);
+            k_bias_sum<float><<<(N + 63) / 64, kThreads, 0, st>>>(part, parts, N, (float*)grad_bias);
         else
-            k_colsum<bf16><<<(N + 63) / 64, 64, 0, st>>>((const bf16*)workspace, M, N, (bf16*)grad_bias);
+            k_bias_sum<bf16><<<(N + 63) / 64, kThreads, 0, st>>>(part, parts, N, (bf16*)grad_bias);
     }
-    if (grad_x)
-        launch_gemm({workspace, weight, N, 1, 1, K, M, K, N, nullptr, nullptr, 0, grad_x, nullptr}, dtype, dtype, st);
-    if (grad_weight)
-        launch_gemm({workspace, x, 1, N, 1, K, N, K, M, nullptr, nullptr, 0, grad_weight, nullptr}, dtype, dtype, st);
+    if (grad_x) {
+        launch_slope({weight, nullptr, 0, N, K, nullptr, ws + lay.wt, 0, lay.np, nullptr}, dtype, dtype, st);
+        launch_gemm({as_is ? grad_out : ws + lay.dz, ws + lay.wt, lay.np, lay.np, M, K, (int)lay.np, nullptr, nullptr, 0, grad_x, nullptr, 0},
+                    dtype, dtype, st);
+    }
+    if (grad_weight) {
+        launch_slope({x, nullptr, 0, M, K, nullptr, ws + lay.xt, 0, lay.mp, nullptr}, dtype, dtype, st);
+        launch_gemm({ws + lay.dzt, ws + lay.xt, lay.mp, lay.mp, N, K, (int)lay.mp, nullptr, nullptr, 0, grad_weight, nullptr, 0},
+                    dtype, dtype, st);
+    }
     return launched();
 }

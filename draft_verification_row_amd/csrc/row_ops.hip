@@ -29,7 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnroll = 4;                       // 16-byte loads per thread and tile
 constexpr int kTileVecs = kThreads * kUnroll;    // 16 KiB
-constexpr int kMaxParts = 64;                     // workgroups per row: one record a lane
+constexpr int kMaxParts = 32;                     // workgroups per row, at most one a lane
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -779,8 +779,12 @@ inline bool ws_ok(const void* p, size_t bytes, size_t need) {
 }
 
 // How a row is split: over as many workgroups as it takes to have kGroups in
-// all, of whole 4 KiB steps.
-constexpr int kGroups = 1024;
+// all, of whole 4 KiB steps, and at most kMaxParts.  Kernel us of log probs
+// with kGroups 512 / 256 / 1024: 144 rows of 128256 with 20 alternatives
+// 25.3 / 31.7 / 30.2, 512 rows without 28.6 / 26.7 / 32.1; six rows with 5
+// alternatives in 63 / 43 / 22 parts 13.1 / 11.8 / 11.1, since the fold reads
+// every part's records.
+constexpr int kGroups = 512;
 struct Split {
     int parts, chunk;
 };
