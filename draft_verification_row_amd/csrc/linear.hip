@@ -12,6 +12,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "spec_verify.h"
 
 namespace {
@@ -127,39 +130,35 @@ __device__ inline void get4(const bf16* p, float (&v)[4]) {
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float((i & 1) ? q[i >> 1] & 0xffff0000u : q[i >> 1] << 16);
 }
 
-// Four neighbouring outputs of row m from n on (n % 4 == 0).  whole: N is a
-// multiple of 4 and every array aligned to four elements.
+// Four neighbouring outputs of row m from n on (n % 4 == 0), one by one.
 template <typename T, typename O>
-__device__ inline void finish4(const Gemm& g, int m, int n, bool whole, float (&z)[4]) {
+__device__ inline void finish4(const Gemm& g, int m, int n, const float (&z)[4]) {
     const size_t at = (size_t)m * g.N + n;
-    const T* bias = static_cast<const T*>(g.bias);
-    T* pre = static_cast<T*>(g.preact);
-    const O* res = static_cast<const O*>(g.residual);
-    O* out = static_cast<O*>(g.out);
-    if (whole) {
-        float v[4];
-        if (bias) {
-            get4(bias + n, v);
-            for (int i = 0; i < 4; ++i) z[i] += v[i];
-        }
-        if (pre) put4(pre + at, z);
-        for (int i = 0; i < 4; ++i) z[i] = act_of(z[i], g.act);
-        if (res) {
-            get4(res + at, v);
-            for (int i = 0; i < 4; ++i) z[i] += v[i];
-        }
-        put4(out + at, z);
-        return;
-    }
     for (int i = 0; i < 4; ++i) {
         if (n + i >= g.N) break;
         float v = z[i];
-        if (bias) v += to_f(bias[n + i]);
-        if (pre) put(pre + at + i, v);
+        if (g.bias) v += to_f(static_cast<const T*>(g.bias)[n + i]);
+        if (g.preact) put(static_cast<T*>(g.preact) + at + i, v);
         v = act_of(v, g.act);
-        if (res) v += to_f(res[at + i]);
-        put(out + at + i, v);
+        if (g.residual) v += to_f(static_cast<const O*>(g.residual)[at + i]);
+        put(static_cast<O*>(g.out) + at + i, v);
     }
+}
+// The same at once, bias (or 0) and residual read before.  Where N is a
+// multiple of 4 and every array aligned to four elements.
+template <typename T, typename O>
+__device__ inline void finish4_whole(const Gemm& g, int m, int n, const float (&bias)[4], const float (&res)[4], float (&z)[4]) {
+    const size_t at = (size_t)m * g.N + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] += bias[i];
+    if (g.preact) put4(static_cast<T*>(g.preact) + at, z);
+    if (g.act != SPEC_ACT_NONE)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = act_of(z[i], g.act);
+    if (g.residual)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] += res[i];
+    put4(static_cast<O*>(g.out) + at, z);
 }
 template <typename T, typename O>
 __device__ inline bool four_at_once(const Gemm& g) {
@@ -168,13 +167,13 @@ __device__ inline bool four_at_once(const Gemm& g) {
 }
 
 // -------------------------------------------------------------- tiled product
-// BM x BN outputs per workgroup of four waves, two by two; a wave has
-// (BM/2) x (BN/2) in 32 x 32 blocks, weights as the instruction's first
-// operand, so that a lane ends with four neighbouring n of one m.  The rows'
-// next 128 bytes (64 bf16, 32 fp32) are one stage in LDS: chunk c of row r lies
-// at place c ^ (r & 7) of its row, which spreads the 32 rows a wave reads
-// at one chunk over all banks.
-constexpr int kRowBytes = 128, kRowChunks = kRowBytes / 16;
+// BM x BN outputs per workgroup of four waves; a wave has WM x WN of them in
+// 32 x 32 blocks, weights as the instruction's first operand, so that a lane
+// ends with four neighbouring n of one m.  The rows'
+// next kRowBytes (128: 64 bf16, 32 fp32) are one stage in LDS: chunk c of row r
+// lies at place c ^ (r / 2 & 7) of its 128 bytes, or c ^ (r / 4 & 3) of its 64,
+// so that sixteen rows read at one chunk use each of the 64 banks once (with
+// c ^ (r & 7) a third of the LDS cycles were conflicts).
 
 // Consecutive workgroups go to different XCDs (blockIdx % 8); each XCD takes a
 // run of neighbouring tiles instead, in columns of kGroupM tiles along m, so
@@ -189,18 +188,27 @@ __device__ inline void tile_of(int id, int count, int tiles_m, int tiles_n, int&
     tn = in / high;
 }
 
-// 16 bytes a lane from the buffer straight to LDS at base + lane * 16.
-__device__ inline void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, uint32_t voffset, uint32_t soffset) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voffset), "s"(rsrc), "s"(soffset) : "memory");
+// 16 bytes a lane from the buffer straight to LDS at base + AT + lane * 16.
+template <int AT>
+__device__ inline void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t base, uint32_t voffset, uint32_t soffset) {
+    asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(base), "v"(voffset), "s"(rsrc), "s"(soffset), "n"(AT) : "memory", "scc");
+}
+template <int... I, typename F>
+__device__ inline void each(std::integer_sequence<int, I...>, F f) {
+    (f(std::integral_constant<int, I>()), ...);
 }
 
-template <typename T, typename O, int BM, int BN, int STAGES, bool DIRECT>
+template <typename T, typename O, int BM, int BN, int WM, int WN, int kRowBytes, int STAGES, bool DIRECT>
 __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
-    constexpr int kElems = 16 / (int)sizeof(T), kStep = kElems * kRowChunks;
-    constexpr int FM = BM / 64, FN = BN / 64;       // 32 x 32 blocks a wave
+    static_assert(BM / WM * (BN / WN) == kThreads / 64, "four waves");
+    constexpr int kRowChunks = kRowBytes / 16, kElems = 16 / (int)sizeof(T), kStep = kElems * kRowChunks;
+    constexpr int kSlab = 1024 / kRowBytes;         // rows of one load
+    constexpr int FM = WM / 32, FN = WN / 32;       // 32 x 32 blocks a wave
+    constexpr int kWavesN = BN / WN;
     constexpr int kRows = BM + BN;                  // rows of a stage: W's, then X's
-    constexpr int kLoads = kRows / 8 / 4;           // 1 KiB loads a wave and stage
+    constexpr int kLoads = kRows / kSlab / 4;       // 1 KiB loads a wave and stage
+    static_assert(kLoads * kSlab * 4 == kRows && BN % (4 * kSlab) == 0, "whole loads, each of one matrix");
     constexpr int kStageBytes = kRows * kRowBytes;
     __shared__ __attribute__((aligned(1024))) char lds[STAGES][kStageBytes];
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -211,9 +219,11 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
     const T* W = static_cast<const T*>(g.W) + (int64_t)n0 * g.ldw;
     const T* X = static_cast<const T*>(g.X) + (int64_t)m0 * g.ldx;
 
-    // load i of this wave: eight rows, lane / 8 the row and lane % 8 the place
-    const int r8 = lane >> 3, c8 = (lane & 7) ^ r8;  // rows start at multiples of 8
-    auto row_of = [&](int i) { return (i * 4 + w) * 8; };
+    // Load i of this wave: kSlab rows, a lane's row and place by its number.
+    // swizzle(r): what a row's chunks are exchanged by; the same for r + 16.
+    auto swizzle = [](int r) { return kRowBytes == 128 ? r >> 1 & 7 : r >> 2 & 3; };
+    auto row_of = [&](int i) { return (i * 4 + w) * kSlab; };
+    const int r8 = lane / kRowChunks, c8 = lane % kRowChunks ^ swizzle(w * kSlab + r8);
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(W), (short)0, 0x7fffffff, 0x00020000);
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(X), (short)0, 0x7fffffff, 0x00020000);
     uint32_t off[kLoads];
@@ -224,14 +234,16 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
         const int64_t e = row_of(i) < BN ? min(r, g.N - 1 - n0) * g.ldw : min(r - BN, g.M - 1 - m0) * g.ldx;
         off[i] = (uint32_t)(e * (int64_t)sizeof(T)) + (uint32_t)c8 * 16;
     }
-    auto load_direct = [&](int stage, int step) {
-        const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&lds[stage][0];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = row_of(i);
-            to_lds(i * 32 < BN ? rw : rx, base + r * kRowBytes, off[i], (uint32_t)step * kRowBytes);
-        }
+    // loads [FROM, TO) of a step into a stage
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&lds[0][0] + w * 1024;
+    auto load_direct = [&](int stage, int step, auto from, auto to) {
+        const uint32_t base = lds0 + stage * kStageBytes, k = (uint32_t)step * kRowBytes;
+        each(std::make_integer_sequence<int, kLoads>(), [&](auto i) {
+            if constexpr (i >= from && i < to) to_lds<i * 4096>(i * 4 * kSlab < BN ? rw : rx, base, off[i], k);
+        });
     };
+    using Zero = std::integral_constant<int, 0>;
+    using All = std::integral_constant<int, kLoads>;
     auto fetch = [&](int step, u32x4 (&q)[kLoads]) {  // the same through registers, any alignment
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -247,45 +259,109 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
     };
 
     f32x16 acc[FN][FM] = {};
-    const int wn = (w & 1) * (BN / 2), wm = (w >> 1) * (BM / 2), l = lane & 31, h = lane >> 5;
-    auto compute = [&](int stage) {
-        const char* s = &lds[stage][0];
+    const int wn = w % kWavesN * WN, wm = w / kWavesN * WM, l = lane & 31, h = lane >> 5;
+    // Operands of one pair of chunks, read from LDS a pair ahead of their use.
+    constexpr int kPairs = kRowChunks / 2, kProducts = FN * FM, kReads = FN + FM;
+    struct Operands {
+        u32x4 a[FN], b[FM];
+    };
+    Operands f[2];
+    const char *as = &lds[0][0] + (wn + l) * kRowBytes, *bs = &lds[0][0] + (BN + wm + l) * kRowBytes;
+    auto read = [&](int stage, int pair, int i, Operands& o) {
+        const int at = stage * kStageBytes + ((2 * pair + h) ^ swizzle(l)) * 16;
+        if (i < FM)
+            o.b[i] = *reinterpret_cast<const u32x4*>(bs + at + i * 32 * kRowBytes);
+        else
+            o.a[i - FM] = *reinterpret_cast<const u32x4*>(as + at + (i - FM) * 32 * kRowBytes);
+    };
+    // The products of one pair, with `between` called for each before it: the
+    // order is kept, so that reads and loads sit under the products.
+    auto multiply = [&](const Operands& o, auto&& between) {
+        each(std::make_integer_sequence<int, kProducts>(), [&](auto i) {
+            between(i);
+            acc[i / FM][i % FM] = mfma32(T(), o.a[i / FM], o.b[i % FM], acc[i / FM][i % FM]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // the next pair's operands are read under the first products
+    auto read_under = [&](auto i, int stage, int pair, Operands& o) {
+        constexpr int from = kProducts > kReads ? (i < kReads ? i : kReads) : i * kReads / kProducts;
+        constexpr int to = kProducts > kReads ? (i + 1 < kReads ? i + 1 : kReads) : (i + 1) * kReads / kProducts;
 #pragma unroll
-        for (int k = 0; k < kRowChunks / 2; ++k) {
-            u32x4 a[FN], b[FM];
-            const int place_at = ((2 * k + h) ^ (l & 7)) * 16;
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-                a[i] = *reinterpret_cast<const u32x4*>(s + (wn + i * 32 + l) * kRowBytes + place_at);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-                b[i] = *reinterpret_cast<const u32x4*>(s + (BN + wm + i * 32 + l) * kRowBytes + place_at);
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int j = 0; j < FM; ++j) acc[i][j] = mfma32(T(), a[i], b[j], acc[i][j]);
-        }
+        for (int r = from; r < to; ++r) read(stage, pair, r, o);
     };
 
     const int steps = (g.K + kStep - 1) / kStep, full = DIRECT ? g.K / kStep : 0;
     if constexpr (DIRECT) {
-        // STAGES - 1 steps are on their way while one is worked on
+        static_assert(kPairs % 2 == 0, "operands alternate");
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
-            if (s < full) load_direct(s, s);
-        for (int s = 0; s < full; ++s) {
-            if (s + STAGES - 1 <= full)
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(kLoads * (STAGES - 2)) : "memory");
-            else
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            // every wave's part of stage s has arrived, and no wave still
-            // reads the stage that is loaded next
+        for (int s = 0; s < STAGES; ++s)
+            if (s < full) load_direct(s, s, Zero(), All());
+        if (full >= STAGES)
+            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(kLoads * (STAGES - 1)) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        int slot = 0;
+        // All but the last pair of a stage.  LOADS: with the second half of the
+        // loads of `step` into the stage that was freed last.
+        auto inner = [&](auto loads, int freed, int step) {
+            each(std::make_integer_sequence<int, kPairs - 1>(), [&](auto p) {
+                multiply(f[p & 1], [&](auto i) {
+                    read_under(i, slot, p + 1, f[(p + 1) & 1]);
+                    if constexpr (loads && p == 0) {
+                        constexpr int h = kLoads / 2, m = kLoads - h;
+                        load_direct(freed, step, std::integral_constant<int, h + i * m / kProducts>(),
+                                    std::integral_constant<int, h + (i + 1) * m / kProducts>());
+                    }
+                });
+            });
+        };
+        // A stage's last pair and the next stage's others.  Before it the next
+        // stage's loads have arrived, in every wave, and every wave has this
+        // stage's last operands, so that it can be filled anew: half of the
+        // loads under this pair, half under the next (an instruction takes
+        // four cycles of a product's 32, so a product hides seven).
+        auto advance = [&](auto loads, int step) {
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            if (s + STAGES - 1 < full) load_direct((s + STAGES - 1) % STAGES, s + STAGES - 1);
-            compute(s % STAGES);
+            const int freed = slot;
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            multiply(f[1], [&](auto i) {
+                read_under(i, slot, 0, f[0]);
+                if constexpr (loads) {
+                    constexpr int h = kLoads / 2;
+                    load_direct(freed, step, std::integral_constant<int, i * h / kProducts>(),
+                                std::integral_constant<int, (i + 1) * h / kProducts>());
+                }
+            });
+            inner(loads, freed, step);
+        };
+        if (full > 0) {
+#pragma unroll
+            for (int i = 0; i < kReads; ++i) read(0, 0, i, f[0]);
+            inner(std::false_type(), 0, 0);
+            int s = STAGES;
+            for (; s < full; ++s) {
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(kLoads * (STAGES - 2)) : "memory");
+                advance(std::true_type(), s);
+            }
+            for (s = s - STAGES + 1; s < full; ++s) {
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                advance(std::false_type(), 0);
+            }
+            multiply(f[1], [](auto) {});
         }
     }
+    auto compute = [&](int stage) {
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) {
+#pragma unroll
+            for (int i = 0; i < kReads; ++i) read(stage, p, i, f[0]);
+            multiply(f[0], [](auto) {});
+        }
+    };
     for (int s = full; s < steps; ++s) {
         u32x4 q[kLoads];
         fetch(s, q);
@@ -297,13 +373,14 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
 
     // Each wave turns its blocks, 32 rows of m at a time, through its own part
     // of the LDS, so that neighbouring lanes have neighbouring n.
-    constexpr int kCols = BN / 2, kPitch = kCols + 4;
+    constexpr int kCols = WN, kPitch = kCols + 4;
     static_assert(4 * 32 * kPitch * 4 <= STAGES * kStageBytes, "the epilogue's tiles fit");
     __syncthreads();
     float* turn = reinterpret_cast<float*>(&lds[0][0]) + w * 32 * kPitch;
     const bool whole = four_at_once<T, O>(g);
-#pragma unroll
-    for (int j = 0; j < FM; ++j) {
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (whole && g.bias) get4(static_cast<const T*>(g.bias) + min(n0 + wn + lane % (WN / 4) * 4, g.N - 4), bias);
+    each(std::make_integer_sequence<int, FM>(), [&](auto j) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -311,15 +388,123 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
                 *reinterpret_cast<f32x4*>(turn + l * kPitch + i * 32 + q * 8 + h * 4) =
                     (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        constexpr int kLanes = kCols / 4, kAtOnce = 64 / kLanes;
+        constexpr int kLanes = kCols / 4, kAtOnce = 64 / kLanes, kBatch = 32 / kAtOnce < 8 ? 32 / kAtOnce : 8;
         const int n = n0 + wn + lane % kLanes * 4;
-        for (int r = lane / kLanes; r < 32; r += kAtOnce) {
-            const int m = m0 + wm + j * 32 + r;
-            const f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * kPitch + lane % kLanes * 4);
-            float z[4] = {v[0], v[1], v[2], v[3]};
-            if (m < g.M && n < g.N) finish4<T, O>(g, m, n, whole, z);
+        const int top = m0 + wm + j * 32;
+        if (n < g.N && whole) {
+#pragma unroll 1
+            for (int r0 = lane / kLanes; r0 < 32; r0 += kAtOnce * kBatch) {
+                // a batch of rows, so that their reads are on their way together
+                float z[kBatch][4], res[kBatch][4];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int r = r0 + u * kAtOnce;
+                    if (g.residual) get4(static_cast<const O*>(g.residual) + (size_t)min(top + r, g.M - 1) * g.N + n, res[u]);
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * kPitch + lane % kLanes * 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[u][i] = v[i];
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int m = top + r0 + u * kAtOnce;
+                    if (m < g.M) finish4_whole<T, O>(g, m, n, bias, res[u], z[u]);
+                }
+            }
+        } else if (n < g.N) {
+#pragma unroll 1
+            for (int r = lane / kLanes; r < 32; r += kAtOnce) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * kPitch + lane % kLanes * 4);
+                const float z[4] = {v[0], v[1], v[2], v[3]};
+                if (top + r < g.M) finish4<T, O>(g, top + r, n, z);
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    });
+}
+
+// -------------------------------------------------------- product of few rows
+// M <= 16 MC: bound by reading W once.  A workgroup has 16 NR rows of W; its
+// four waves take every fourth piece of KS * 64 bytes of the rows, W and X
+// straight into registers as operands of 16x16 instructions (lane l: row
+// l % 16, chunk l / 16), the next piece on its way while one is multiplied.
+// The waves' sums are added in LDS.
+__device__ inline f32x4 mfma16(bf16, u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ inline f32x4 mfma16(float, u32x4 a, u32x4 b, f32x4 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], c, 0, 0, 0);
+    return c;
+}
+
+template <typename T, typename O, int MC, int NR, bool ALIGNED>
+__global__ __launch_bounds__(kThreads) void k_few(Gemm g) {
+    constexpr int kElems = 16 / (int)sizeof(T), KS = MC * NR >= 8 ? 2 : 4, kPiece = KS * 4 * kElems;
+    constexpr int kPitch = 16 * NR + 4;
+    __shared__ float sums[4][16 * MC][kPitch];
+    const int t = threadIdx.x, lane = t & 63, w = t >> 6, r = lane & 15, c = lane >> 4;
+    const int n0 = blockIdx.x * 16 * NR;
+    const T *W[NR], *X[MC];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) W[i] = static_cast<const T*>(g.W) + min(n0 + i * 16 + r, g.N - 1) * g.ldw;
+#pragma unroll
+    for (int j = 0; j < MC; ++j) X[j] = static_cast<const T*>(g.X) + min(j * 16 + r, g.M - 1) * g.ldx;
+    struct Piece {
+        u32x4 a[KS][NR], b[KS][MC];
+    };
+    auto load = [&](int p, Piece& q) {
+        const bool full = ALIGNED && (p + 1) * kPiece <= g.K;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int k = p * kPiece + (s * 4 + c) * kElems;
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+                q.a[s][i] = full ? *reinterpret_cast<const u32x4*>(W[i] + k) : chunk_of(W[i], k, g.K);
+#pragma unroll
+            for (int j = 0; j < MC; ++j) {
+                q.b[s][j] = (u32x4){0, 0, 0, 0};
+                if (j * 16 + r < g.M)
+                    q.b[s][j] = full ? *reinterpret_cast<const u32x4*>(X[j] + k) : chunk_of(X[j], k, g.K);
+            }
+        }
+    };
+    f32x4 acc[NR][MC] = {};
+    const int pieces = (g.K + kPiece - 1) / kPiece;
+    Piece q;
+    if (w < pieces) load(w, q);
+    for (int p = w; p < pieces; p += 4) {
+        Piece next;
+        if (p + 4 < pieces) load(p + 4, next);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int j = 0; j < MC; ++j) acc[i][j] = mfma16(T(), q.a[s][i], q.b[s][j], acc[i][j]);
+        q = next;
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int j = 0; j < MC; ++j) *reinterpret_cast<f32x4*>(&sums[w][j * 16 + r][i * 16 + c * 4]) = acc[i][j];
+    __syncthreads();
+    const bool whole = four_at_once<T, O>(g);
+    for (int i = t; i < 16 * MC * 4 * NR; i += kThreads) {
+        const int m = i / (4 * NR), n = i % (4 * NR) * 4;
+        f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][m][n]);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) v += *reinterpret_cast<const f32x4*>(&sums[k][m][n]);
+        float z[4] = {v[0], v[1], v[2], v[3]};
+        if (m >= g.M || n0 + n >= g.N) continue;
+        if (whole) {
+            float bias[4] = {0.f, 0.f, 0.f, 0.f}, res[4];
+            if (g.bias) get4(static_cast<const T*>(g.bias) + n0 + n, bias);
+            if (g.residual) get4(static_cast<const O*>(g.residual) + (size_t)m * g.N + n0 + n, res);
+            finish4_whole<T, O>(g, m, n0 + n, bias, res, z);
+        } else {
+            finish4<T, O>(g, m, n0 + n, z);
+        }
     }
 }
 
@@ -397,24 +582,50 @@ inline bool ws_ok(const void* p, size_t bytes, size_t need) {
 }
 inline spec_status launched() { return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP; }
 
-template <typename T, typename O, int B, int STAGES, bool DIRECT>
+template <typename T, typename O, int BM, int BN, int WM, int WN, int kRowBytes, int STAGES, bool DIRECT>
 void launch_tiles(Gemm g, hipStream_t st) {
-    const int tm = (g.M + B - 1) / B;
-    g.tiles_n = (g.N + B - 1) / B;
-    k_gemm<T, O, B, B, STAGES, DIRECT><<<(unsigned)tm * (unsigned)g.tiles_n, kThreads, 0, st>>>(g);
+    const int tm = (g.M + BM - 1) / BM;
+    g.tiles_n = (g.N + BN - 1) / BN;
+    k_gemm<T, O, BM, BN, WM, WN, kRowBytes, STAGES, DIRECT><<<(unsigned)tm * (unsigned)g.tiles_n, kThreads, 0, st>>>(g);
 }
+template <typename T, typename O, int MC, int NR>
+void launch_few(const Gemm& g, bool aligned, hipStream_t st) {
+    const unsigned grid = (unsigned)((g.N + 16 * NR - 1) / (16 * NR));
+    if (aligned)
+        k_few<T, O, MC, NR, true><<<grid, kThreads, 0, st>>>(g);
+    else
+        k_few<T, O, MC, NR, false><<<grid, kThreads, 0, st>>>(g);
+}
+template <typename T, typename O, int MC>
+void launch_few(const Gemm& g, bool aligned, hipStream_t st) {
+    if (g.N >= 64 * 512)
+        launch_few<T, O, MC, 4>(g, aligned, st);
+    else
+        launch_few<T, O, MC, 1>(g, aligned, st);
+}
+
 template <typename T, typename O>
 void launch_typed(const Gemm& g, hipStream_t st) {
     const uintptr_t a = (uintptr_t)g.X | (uintptr_t)g.W | (uintptr_t)(g.ldx * (int64_t)sizeof(T)) | (uintptr_t)(g.ldw * (int64_t)sizeof(T));
     auto tiles = [&](int b) { return (long long)((g.M + b - 1) / b) * ((g.N + b - 1) / b); };
-    if (a % 16 != 0)
-        launch_tiles<T, O, 64, 2, false>(g, st);
+    if (g.M <= 16)
+        launch_few<T, O, 1>(g, a % 16 == 0, st);
+    else if (g.M <= 32 && a % 16 == 0 && g.N >= 16384)
+        launch_tiles<T, O, 32, 128, 32, 32, 128, 4, true>(g, st);
+    else if (g.M <= 64 && g.M > 32 && a % 16 == 0 && g.N >= 16384)
+        launch_tiles<T, O, 64, 128, 64, 32, 128, 3, true>(g, st);
+    else if (g.M <= 32)
+        launch_few<T, O, 2>(g, a % 16 == 0, st);
+    else if (g.M <= 64)
+        launch_few<T, O, 4>(g, a % 16 == 0, st);
+    else if (a % 16 != 0)
+        launch_tiles<T, O, 64, 64, 32, 32, 128, 2, false>(g, st);
     else if (tiles(256) >= 200)
-        launch_tiles<T, O, 256, 2, true>(g, st);
+        launch_tiles<T, O, 256, 256, 128, 128, 128, 2, true>(g, st);
     else if (tiles(128) >= 200)
-        launch_tiles<T, O, 128, 4, true>(g, st);
+        launch_tiles<T, O, 128, 128, 64, 64, 128, 4, true>(g, st);
     else
-        launch_tiles<T, O, 64, 4, true>(g, st);
+        launch_tiles<T, O, 64, 64, 32, 32, 128, 4, true>(g, st);
 }
 void launch_gemm(const Gemm& g, spec_dtype d, spec_dtype o, hipStream_t st) {
     if (d == SPEC_F32)
