@@ -35,11 +35,18 @@ __device__ inline void put(bf16* p, float f) {  // round to nearest even
 }
 
 // ---------------------------------------------------------------- activation
+// 1 / (1 + e^-z) by the hardware's base-2 exponential and reciprocal, each good
+// to a unit in the last place: an epilogue of one wave a SIMD is bound by its
+// instructions (8192 x 4096 x 4096 with silu and residual: 350 us with expf
+// and a division).
+__device__ inline float sigmoid_of(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+}
 __device__ inline float act_of(float z, int act) {
     switch (act) {
         case SPEC_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);
         case SPEC_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-        case SPEC_ACT_SILU: return z / (1.f + expf(-z));
+        case SPEC_ACT_SILU: return z * sigmoid_of(z);
         default: return z;
     }
 }
@@ -47,9 +54,10 @@ __device__ inline float act_slope(float z, int act) {
     switch (act) {
         case SPEC_ACT_RELU: return z > 0.f ? 1.f : 0.f;
         case SPEC_ACT_GELU:
-            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+            return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
+                   z * __builtin_amdgcn_exp2f(-0.72134752044448170368f * z * z) * 0.39894228040143268f;
         case SPEC_ACT_SILU: {
-            const float s = 1.f / (1.f + expf(-z));
+            const float s = sigmoid_of(z);
             return s * fmaf(z, 1.f - s, 1.f);
         }
         default: return 1.f;
@@ -362,13 +370,18 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
             multiply(f[0], [](auto) {});
         }
     };
-    for (int s = full; s < steps; ++s) {
+    // what is no whole step, or not aligned: the next step's loads are on
+    // their way while one is worked on
+    if (full < steps) {
         u32x4 q[kLoads];
-        fetch(s, q);
-        __syncthreads();
-        place(s % STAGES, q);
-        __syncthreads();
-        compute(s % STAGES);
+        fetch(full, q);
+        for (int s = full; s < steps; ++s) {
+            __syncthreads();
+            place(0, q);
+            __syncthreads();
+            if (s + 1 < steps) fetch(s + 1, q);
+            compute(0);
+        }
     }
 
     // Each wave turns its blocks, 32 rows of m at a time, through its own part
@@ -511,7 +524,10 @@ __global__ __launch_bounds__(kThreads) void k_few(Gemm g) {
 // ---------------------------------------------------------- gradients' inputs
 // dz = dy act'(z) to dz [M][ld] and, turned, to dzt [N][ldt], rounded, zero up
 // to the rows' ends; sums of 64 rows' unrounded dz to part [M/64][N].  Each of
-// the three is optional.  The same kernel turns a matrix (dy alone).
+// the three is optional.  The same kernel turns a matrix (dy alone).  Bound by
+// memory: a thread reads and writes eight neighbouring elements at once
+// (VECTOR: N a multiple of 8 and 16-byte aligned inputs; ld and ldt are whole
+// 16-byte chunks always), the turning goes through LDS.
 struct Slope {
     const void *dy, *preact;
     int act, M, N;
@@ -520,50 +536,91 @@ struct Slope {
     float* part;
 };
 
-template <typename I, typename T>
+template <typename I, bool VECTOR>
+__device__ inline void get8(const I* p, int left, float (&v)[8]) {
+    if constexpr (VECTOR) {
+        float a[4], b[4];
+        get4(p, a);
+        get4(p + 4, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = a[i], v[i + 4] = b[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f(p[i]) : 0.f;
+    }
+}
+// eight elements to a row of whole chunks, `left` of which are in it
+template <typename T>
+__device__ inline void put8(T* p, int64_t left, const float (&v)[8]) {
+    constexpr int kElems = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int c = 0; c < 8; c += kElems) {
+        u32x4 q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if constexpr (sizeof(T) == 2)
+                q[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            else
+                q[i] = __float_as_uint(v[c + i]);
+        if (c < left) *reinterpret_cast<u32x4*>(p + c) = q;
+    }
+}
+
+template <typename I, typename T, bool VECTOR>
 __global__ __launch_bounds__(kThreads) void k_slope(Slope a) {
     __shared__ float tile[64][65];
-    const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64, t = threadIdx.x, c = t & 63, r0 = t >> 6;
-    float sum = 0.f;
-    for (int r = r0; r < 64; r += 4) {
-        const int m = m0 + r, n = n0 + c;
-        float v = 0.f;
+    const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64, t = threadIdx.x, c = t % 8 * 8;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int r = t / 8 + u * 32, m = m0 + r, n = n0 + c;
+        float v[8] = {}, z[8];
         if (m < a.M && n < a.N) {
             const size_t at = (size_t)m * a.N + n;
-            v = to_f(static_cast<const I*>(a.dy)[at]);
-            if (a.preact) v *= act_slope(to_f(static_cast<const T*>(a.preact)[at]), a.act);
+            get8<I, VECTOR>(static_cast<const I*>(a.dy) + at, a.N - n, v);
+            if (a.preact) {
+                get8<T, VECTOR>(static_cast<const T*>(a.preact) + at, a.N - n, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= act_slope(z[i], a.act);
+            }
         }
-        sum += v;
-        tile[r][c] = v;
-        if (a.dz && m < a.M && n < a.ld) put(static_cast<T*>(a.dz) + (size_t)m * a.ld + n, v);
+        if (a.dz && m < a.M && n < a.ld) put8(static_cast<T*>(a.dz) + (size_t)m * a.ld + n, a.ld - n, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tile[r][c + i] = v[i];
     }
     __syncthreads();
     if (a.dzt)
-        for (int r = r0; r < 64; r += 4) {
-            const int n = n0 + r, m = m0 + c;
-            if (n < a.N && m < a.ldt) put(static_cast<T*>(a.dzt) + (size_t)n * a.ldt + m, tile[c][r]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = t / 8 + u * 32, n = n0 + r, m = m0 + c;
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = tile[c + i][r];
+            if (n < a.N && m < a.ldt) put8(static_cast<T*>(a.dzt) + (size_t)n * a.ldt + m, a.ldt - m, v);
         }
-    if (a.part) {
-        __shared__ float sums[4][64];
-        sums[r0][c] = sum;
-        __syncthreads();
-        if (r0 == 0 && n0 + c < a.N)
-            a.part[(size_t)blockIdx.y * a.N + n0 + c] = (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]);
+    if (a.part && t < 64 && n0 + t < a.N) {
+        float s[4] = {};
+#pragma unroll
+        for (int r = 0; r < 64; ++r) s[r % 4] += tile[r][t];
+        a.part[(size_t)blockIdx.y * a.N + n0 + t] = (s[0] + s[1]) + (s[2] + s[3]);
     }
 }
 
 // dbias[n] = the sum of the parts, in a fixed order: 64 columns a workgroup,
-// every fourth part to a wave
+// every sixteenth part to a wave
+constexpr int kSumWaves = 16;
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_bias_sum(const float* part, int parts, int N, T* out) {
-    __shared__ float sums[4][64];
+__global__ __launch_bounds__(64 * kSumWaves) void k_bias_sum(const float* part, int parts, int N, T* out) {
+    __shared__ float sums[kSumWaves][64];
     const int c = threadIdx.x & 63, w = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
     float s = 0.f;
     if (n < N)
-        for (int p = w; p < parts; p += 4) s += part[(size_t)p * N + n];
+        for (int p = w; p < parts; p += kSumWaves) s += part[(size_t)p * N + n];
     sums[w][c] = s;
     __syncthreads();
-    if (w == 0 && n < N) put(out + n, (sums[0][c] + sums[1][c]) + (sums[2][c] + sums[3][c]));
+    if (w == 0 && n < N) {
+        for (int i = 1; i < kSumWaves; ++i) s += sums[i][c];
+        put(out + n, s);
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -656,15 +713,21 @@ inline GradLayout grad_layout(spec_dtype d, long long M, long long N, long long 
     return l;
 }
 
-void launch_slope(const Slope& a, spec_dtype in, spec_dtype d, hipStream_t st) {
-    // the turned rows' padding lies under the last blocks too
+template <typename I, typename T>
+void launch_slope(const Slope& a, hipStream_t st) {
     const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
-    if (d == SPEC_F32)
-        k_slope<float, float><<<grid, kThreads, 0, st>>>(a);
-    else if (in == SPEC_F32)
-        k_slope<float, bf16><<<grid, kThreads, 0, st>>>(a);
+    if (a.N % 8 == 0 && ((uintptr_t)a.dy | (uintptr_t)a.preact) % 16 == 0)
+        k_slope<I, T, true><<<grid, kThreads, 0, st>>>(a);
     else
-        k_slope<bf16, bf16><<<grid, kThreads, 0, st>>>(a);
+        k_slope<I, T, false><<<grid, kThreads, 0, st>>>(a);
+}
+void launch_slope(const Slope& a, spec_dtype in, spec_dtype d, hipStream_t st) {
+    if (d == SPEC_F32)
+        launch_slope<float, float>(a, st);
+    else if (in == SPEC_F32)
+        launch_slope<float, bf16>(a, st);
+    else
+        launch_slope<bf16, bf16>(a, st);
 }
 
 }  // namespace
@@ -715,9 +778,9 @@ extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const
         const float* part = reinterpret_cast<const float*>(ws + lay.part);
         const int parts = (M + 63) / 64;
         if (dtype == SPEC_F32)
-            k_bias_sum<float><<<(N + 63) / 64, kThreads, 0, st>>>(part, parts, N, (float*)grad_bias);
+            k_bias_sum<float><<<(N + 63) / 64, 64 * kSumWaves, 0, st>>>(part, parts, N, (float*)grad_bias);
         else
-            k_bias_sum<bf16><<<(N + 63) / 64, kThreads, 0, st>>>(part, parts, N, (bf16*)grad_bias);
+            k_bias_sum<bf16><<<(N + 63) / 64, 64 * kSumWaves, 0, st>>>(part, parts, N, (bf16*)grad_bias);
     }
     if (grad_x) {
         launch_slope({weight, nullptr, 0, N, K, nullptr, ws + lay.wt, 0, lay.np, nullptr}, dtype, dtype, st);
