@@ -534,6 +534,13 @@ struct Slope {
     void *dz, *dzt;
     int64_t ld, ldt;
     float* part;
+    bool vector;
+};
+// Up to three of them in one launch: dz, then W and x turned (jobs 1 and 2 are
+// of the operands' type).  A job's 64 x 64 blocks follow the last one's.
+struct Slopes {
+    Slope job[3];
+    unsigned end[3];  // blocks up to the end of each job
 };
 
 template <typename I, bool VECTOR>
@@ -567,9 +574,9 @@ __device__ inline void put8(T* p, int64_t left, const float (&v)[8]) {
 }
 
 template <typename I, typename T, bool VECTOR>
-__global__ __launch_bounds__(kThreads) void k_slope(Slope a) {
-    __shared__ float tile[64][65];
-    const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64, t = threadIdx.x, c = t % 8 * 8;
+__device__ inline void slope_block(const Slope& a, unsigned block, float (&tile)[64][65]) {
+    const unsigned across = (unsigned)((a.N + 63) / 64), row = block / across;
+    const int n0 = (int)(block % across) * 64, m0 = (int)row * 64, t = threadIdx.x, c = t % 8 * 8;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const int r = t / 8 + u * 32, m = m0 + r, n = n0 + c;
@@ -601,7 +608,26 @@ __global__ __launch_bounds__(kThreads) void k_slope(Slope a) {
         float s[4] = {};
 #pragma unroll
         for (int r = 0; r < 64; ++r) s[r % 4] += tile[r][t];
-        a.part[(size_t)blockIdx.y * a.N + n0 + t] = (s[0] + s[1]) + (s[2] + s[3]);
+        a.part[(size_t)row * a.N + n0 + t] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+}
+
+template <typename I, typename T>
+__global__ __launch_bounds__(kThreads) void k_slopes(Slopes a) {
+    __shared__ float tile[64][65];
+    const unsigned b = blockIdx.x;
+    if (b < a.end[0]) {
+        if (a.job[0].vector)
+            slope_block<I, T, true>(a.job[0], b, tile);
+        else
+            slope_block<I, T, false>(a.job[0], b, tile);
+    } else {
+        const bool last = b >= a.end[1];
+        const Slope& s = a.job[last ? 2 : 1];
+        if (s.vector)
+            slope_block<T, T, true>(s, b - a.end[last ? 1 : 0], tile);
+        else
+            slope_block<T, T, false>(s, b - a.end[last ? 1 : 0], tile);
     }
 }
 
@@ -627,7 +653,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_bias_sum(const float* part, 
 inline bool types_ok(spec_dtype d, spec_dtype o) {
     return d == SPEC_BF16 ? (o == SPEC_BF16 || o == SPEC_F32) : d == SPEC_F32 && o == SPEC_F32;
 }
-constexpr long long kMaxElems = 1ll << 35;
+constexpr long long kMaxElems = 1ll << 34;  // of a matrix: launches stay below 2^32 threads
 inline bool sizes_ok(long long M, long long N, long long K) {
     return M >= 1 && N >= 1 && K >= 1 && M <= SPEC_MAX_LINEAR && N <= SPEC_MAX_LINEAR && K <= SPEC_MAX_LINEAR &&
            M * N < kMaxElems && M * K < kMaxElems && N * K < kMaxElems;
@@ -713,21 +739,21 @@ inline GradLayout grad_layout(spec_dtype d, long long M, long long N, long long 
     return l;
 }
 
-template <typename I, typename T>
-void launch_slope(const Slope& a, hipStream_t st) {
-    const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
-    if (a.N % 8 == 0 && ((uintptr_t)a.dy | (uintptr_t)a.preact) % 16 == 0)
-        k_slope<I, T, true><<<grid, kThreads, 0, st>>>(a);
-    else
-        k_slope<I, T, false><<<grid, kThreads, 0, st>>>(a);
-}
-void launch_slope(const Slope& a, spec_dtype in, spec_dtype d, hipStream_t st) {
+void launch_slopes(Slopes& a, spec_dtype in, spec_dtype d, hipStream_t st) {
+    unsigned blocks = 0;
+    for (int i = 0; i < 3; ++i) {
+        Slope& s = a.job[i];
+        s.vector = s.N % 8 == 0 && ((uintptr_t)s.dy | (uintptr_t)s.preact) % 16 == 0;
+        if (s.dz || s.dzt || s.part) blocks += (unsigned)((s.N + 63) / 64) * (unsigned)((s.M + 63) / 64);
+        a.end[i] = blocks;
+    }
+    if (blocks == 0) return;
     if (d == SPEC_F32)
-        launch_slope<float, float>(a, st);
+        k_slopes<float, float><<<blocks, kThreads, 0, st>>>(a);
     else if (in == SPEC_F32)
-        launch_slope<float, bf16>(a, st);
+        k_slopes<float, bf16><<<blocks, kThreads, 0, st>>>(a);
     else
-        launch_slope<bf16, bf16>(a, st);
+        k_slopes<bf16, bf16><<<blocks, kThreads, 0, st>>>(a);
 }
 
 }  // namespace
@@ -770,10 +796,13 @@ extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const
     // without an activation dy is dz where it has the operands' type and
     // aligned rows
     const bool as_is = !z && dtype == out_dtype && lay.np == N && (uintptr_t)grad_out % 16 == 0;
-    const Slope s{grad_out, z, activation, M, N, grad_x && !as_is ? ws + lay.dz : nullptr,
-                  grad_weight ? ws + lay.dzt : nullptr, lay.np, lay.mp,
-                  grad_bias ? reinterpret_cast<float*>(ws + lay.part) : nullptr};
-    if (s.dz || s.dzt || s.part) launch_slope(s, out_dtype, dtype, st);
+    Slopes s{};
+    s.job[0] = {grad_out, z, activation, M, N, grad_x && !as_is ? ws + lay.dz : nullptr,
+                grad_weight ? ws + lay.dzt : nullptr, lay.np, lay.mp,
+                grad_bias ? reinterpret_cast<float*>(ws + lay.part) : nullptr, false};
+    if (grad_x) s.job[1] = {weight, nullptr, 0, N, K, nullptr, ws + lay.wt, 0, lay.np, nullptr, false};
+    if (grad_weight) s.job[2] = {x, nullptr, 0, M, K, nullptr, ws + lay.xt, 0, lay.mp, nullptr, false};
+    launch_slopes(s, out_dtype, dtype, st);
     if (grad_bias) {
         const float* part = reinterpret_cast<const float*>(ws + lay.part);
         const int parts = (M + 63) / 64;
@@ -782,15 +811,11 @@ extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const
         else
             k_bias_sum<bf16><<<(N + 63) / 64, 64 * kSumWaves, 0, st>>>(part, parts, N, (bf16*)grad_bias);
     }
-    if (grad_x) {
-        launch_slope({weight, nullptr, 0, N, K, nullptr, ws + lay.wt, 0, lay.np, nullptr}, dtype, dtype, st);
+    if (grad_x)
         launch_gemm({as_is ? grad_out : ws + lay.dz, ws + lay.wt, lay.np, lay.np, M, K, (int)lay.np, nullptr, nullptr, 0, grad_x, nullptr, 0},
                     dtype, dtype, st);
-    }
-    if (grad_weight) {
-        launch_slope({x, nullptr, 0, M, K, nullptr, ws + lay.xt, 0, lay.mp, nullptr}, dtype, dtype, st);
+    if (grad_weight)
         launch_gemm({ws + lay.dzt, ws + lay.xt, lay.mp, lay.mp, N, K, (int)lay.mp, nullptr, nullptr, 0, grad_weight, nullptr, 0},
                     dtype, dtype, st);
-    }
     return launched();
 }

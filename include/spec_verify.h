@@ -568,7 +568,7 @@ spec_status spec_draft_kl_grad(const void *target_logits, const void *draft_logi
  *                activation needs
  * dtype SPEC_BF16 takes either out_dtype, SPEC_F32 only SPEC_F32 (else
  * SPEC_EDTYPE).  Gelu is z Phi(z) with the normal distribution function.
- * 1 <= M, N, K <= SPEC_MAX_LINEAR, and M * N, M * K and N * K below 2^35.
+ * 1 <= M, N, K <= SPEC_MAX_LINEAR, and M * N, M * K and N * K below 2^34.
  * The workspace needs no initialization and is left with any contents: it is
  * not one of the zero-filled ones above.
  */

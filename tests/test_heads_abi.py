@@ -117,16 +117,18 @@ def test_binding_refuses_host_tensors():
 def test_a_capture_refuses_leaves_of_another_streams_graph():
     """The rule behind captured backward passes, on the host: streams are
     numbers here."""
-    from draft_verification_row_amd.heads import _leaf_nodes
+    from draft_verification_row_amd.heads import _note_stream
     x, y = torch.ones(3, requires_grad=True), torch.ones(3)
-    graph = (x * y, _leaf_nodes(1, False, [x, y, None, x * 2]))
-    assert len(graph[1]) == 1
-    assert _leaf_nodes(2, False, [x])            # eager calls may use any stream
-    assert _leaf_nodes(1, True, [x])             # a capture on the same one too
+    graph = x * y
+    _note_stream(graph.grad_fn.next_functions, 1, False)
+    again = x * 2
+    _note_stream(again.grad_fn.next_functions, 2, False)   # eager calls may use any stream
+    _note_stream(again.grad_fn.next_functions, 1, True)    # a capture on the same one too
     with pytest.raises(sv.SpecVerifyError):
-        _leaf_nodes(2, True, [x])
-    del graph
-    assert _leaf_nodes(2, True, [x])             # the graph is gone
+        _note_stream(again.grad_fn.next_functions, 2, True)
+    _note_stream((again * 3).grad_fn.next_functions, 2, True)  # no leaf
+    del graph, again
+    _note_stream((x * 2).grad_fn.next_functions, 2, True)  # the graphs are gone
 
 
 @pytest.mark.gpu
