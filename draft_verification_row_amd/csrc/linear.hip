@@ -74,7 +74,8 @@ struct Gemm {
     const void *bias, *residual;
     int act;
     void *out, *preact;
-    int tiles_n;
+    int tiles_n, splits;  // splits of K, and where there are several
+    float* part;          // their sums [splits][M][N]
 };
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -138,6 +139,12 @@ __device__ inline void get4(const bf16* p, float (&v)[4]) {
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float((i & 1) ? q[i >> 1] & 0xffff0000u : q[i >> 1] << 16);
 }
 
+// Four values as they lie in memory, so that a load ahead of its use stays one.
+template <typename O>
+using Raw4 = std::conditional_t<sizeof(O) == 2, u32x2, f32x4>;
+__device__ inline float raw4_at(u32x2 q, int i) { return __uint_as_float((i & 1) ? q[i >> 1] & 0xffff0000u : q[i >> 1] << 16); }
+__device__ inline float raw4_at(f32x4 q, int i) { return q[i]; }
+
 // Four neighbouring outputs of row m from n on (n % 4 == 0), one by one.
 template <typename T, typename O>
 __device__ inline void finish4(const Gemm& g, int m, int n, const float (&z)[4]) {
@@ -155,7 +162,7 @@ __device__ inline void finish4(const Gemm& g, int m, int n, const float (&z)[4])
 // The same at once, bias (or 0) and residual read before.  Where N is a
 // multiple of 4 and every array aligned to four elements.
 template <typename T, typename O>
-__device__ inline void finish4_whole(const Gemm& g, int m, int n, const float (&bias)[4], const float (&res)[4], float (&z)[4]) {
+__device__ inline void finish4_whole(const Gemm& g, int m, int n, const float (&bias)[4], Raw4<O> res, float (&z)[4]) {
     const size_t at = (size_t)m * g.N + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i) z[i] += bias[i];
@@ -165,7 +172,7 @@ __device__ inline void finish4_whole(const Gemm& g, int m, int n, const float (&
         for (int i = 0; i < 4; ++i) z[i] = act_of(z[i], g.act);
     if (g.residual)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] += res[i];
+        for (int i = 0; i < 4; ++i) z[i] += raw4_at(res, i);
     put4(static_cast<O*>(g.out) + at, z);
 }
 template <typename T, typename O>
@@ -197,10 +204,15 @@ __device__ inline void tile_of(int id, int count, int tiles_m, int tiles_n, int&
 }
 
 // 16 bytes a lane from the buffer straight to LDS at base + AT + lane * 16.
-template <int AT>
+// NT: read once, not to be kept in the caches.
+template <int AT, bool NT>
 __device__ inline void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t base, uint32_t voffset, uint32_t soffset) {
-    asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(base), "v"(voffset), "s"(rsrc), "s"(soffset), "n"(AT) : "memory", "scc");
+    if constexpr (NT)
+        asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+                     :: "s"(base), "v"(voffset), "s"(rsrc), "s"(soffset), "n"(AT) : "memory", "scc");
+    else
+        asm volatile("s_add_u32 m0, %0, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :: "s"(base), "v"(voffset), "s"(rsrc), "s"(soffset), "n"(AT) : "memory", "scc");
 }
 template <int... I, typename F>
 __device__ inline void each(std::integer_sequence<int, I...>, F f) {
@@ -208,7 +220,7 @@ __device__ inline void each(std::integer_sequence<int, I...>, F f) {
 }
 
 template <typename T, typename O, int BM, int BN, int WM, int WN, int kRowBytes, int STAGES, bool DIRECT>
-__global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
+__global__ __launch_bounds__(kThreads, (BM + BN) * kRowBytes * STAGES <= 80 * 1024 ? 2 : 1) void k_gemm(Gemm g) {
     static_assert(BM / WM * (BN / WN) == kThreads / 64, "four waves");
     constexpr int kRowChunks = kRowBytes / 16, kElems = 16 / (int)sizeof(T), kStep = kElems * kRowChunks;
     constexpr int kSlab = 1024 / kRowBytes;         // rows of one load
@@ -222,7 +234,8 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     int tm, tn;
     const int tiles_m = (g.M + BM - 1) / BM;
-    tile_of(blockIdx.x, gridDim.x, tiles_m, g.tiles_n, tm, tn);
+    const int tiles = tiles_m * g.tiles_n, split = blockIdx.x / tiles;
+    tile_of(blockIdx.x % tiles, tiles, tiles_m, g.tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const T* W = static_cast<const T*>(g.W) + (int64_t)n0 * g.ldw;
     const T* X = static_cast<const T*>(g.X) + (int64_t)m0 * g.ldx;
@@ -242,12 +255,16 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
         const int64_t e = row_of(i) < BN ? min(r, g.N - 1 - n0) * g.ldw : min(r - BN, g.M - 1 - m0) * g.ldx;
         off[i] = (uint32_t)(e * (int64_t)sizeof(T)) + (uint32_t)c8 * 16;
     }
+    // this split's steps [begin, end), `full` of them whole and loaded directly
+    const int steps = (g.K + kStep - 1) / kStep, per = (steps + g.splits - 1) / g.splits;
+    const int begin = split * per, end = min(steps, begin + per);
+    const int full = DIRECT ? max(0, min(g.K / kStep, end) - begin) : 0;
     // loads [FROM, TO) of a step into a stage
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&lds[0][0] + w * 1024;
     auto load_direct = [&](int stage, int step, auto from, auto to) {
-        const uint32_t base = lds0 + stage * kStageBytes, k = (uint32_t)step * kRowBytes;
+        const uint32_t base = lds0 + stage * kStageBytes, k = (uint32_t)(begin + step) * kRowBytes;
         each(std::make_integer_sequence<int, kLoads>(), [&](auto i) {
-            if constexpr (i >= from && i < to) to_lds<i * 4096>(i * 4 * kSlab < BN ? rw : rx, base, off[i], k);
+            if constexpr (i >= from && i < to) to_lds<i * 4096, BM <= 64 && BN == 128 && i * 4 * kSlab < BN>(i * 4 * kSlab < BN ? rw : rx, base, off[i], k);
         });
     };
     using Zero = std::integral_constant<int, 0>;
@@ -299,7 +316,6 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
         for (int r = from; r < to; ++r) read(stage, pair, r, o);
     };
 
-    const int steps = (g.K + kStep - 1) / kStep, full = DIRECT ? g.K / kStep : 0;
     if constexpr (DIRECT) {
         static_assert(kPairs % 2 == 0, "operands alternate");
 #pragma unroll
@@ -372,14 +388,14 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
     };
     // what is no whole step, or not aligned: the next step's loads are on
     // their way while one is worked on
-    if (full < steps) {
+    if (begin + full < end) {
         u32x4 q[kLoads];
-        fetch(full, q);
-        for (int s = full; s < steps; ++s) {
+        fetch(begin + full, q);
+        for (int s = begin + full; s < end; ++s) {
             __syncthreads();
             place(0, q);
             __syncthreads();
-            if (s + 1 < steps) fetch(s + 1, q);
+            if (s + 1 < end) fetch(s + 1, q);
             compute(0);
         }
     }
@@ -391,8 +407,19 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
     __syncthreads();
     float* turn = reinterpret_cast<float*>(&lds[0][0]) + w * 32 * kPitch;
     const bool whole = four_at_once<T, O>(g);
+    constexpr int kLanes = kCols / 4, kAtOnce = 64 / kLanes, kBatch = 32 / kAtOnce < 8 ? 32 / kAtOnce : 8;
+    const int n = n0 + wn + lane % kLanes * 4;
     float bias[4] = {0.f, 0.f, 0.f, 0.f};
-    if (whole && g.bias) get4(static_cast<const T*>(g.bias) + min(n0 + wn + lane % (WN / 4) * 4, g.N - 4), bias);
+    Raw4<O> ahead[kBatch];
+    auto look_ahead = [&](int m) {  // the batch of rows from m on
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            ahead[u] = *reinterpret_cast<const Raw4<O>*>(static_cast<const O*>(g.residual) + (size_t)min(m + u * kAtOnce, g.M - 1) * g.N + n);
+    };
+    if (whole && n < g.N && g.splits == 1) {
+        if (g.bias) get4(static_cast<const T*>(g.bias) + n, bias);
+        if (g.residual) look_ahead(m0 + wm + lane / kLanes);
+    }
     each(std::make_integer_sequence<int, FM>(), [&](auto j) {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
@@ -401,22 +428,33 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
                 *reinterpret_cast<f32x4*>(turn + l * kPitch + i * 32 + q * 8 + h * 4) =
                     (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        constexpr int kLanes = kCols / 4, kAtOnce = 64 / kLanes, kBatch = 32 / kAtOnce < 8 ? 32 / kAtOnce : 8;
-        const int n = n0 + wn + lane % kLanes * 4;
         const int top = m0 + wm + j * 32;
-        if (n < g.N && whole) {
+        if (g.splits > 1) {
+#pragma unroll 1
+            for (int r = lane / kLanes; r < 32; r += kAtOnce) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * kPitch + lane % kLanes * 4);
+                if (top + r >= g.M) break;
+                float* to = g.part + ((size_t)split * g.M + top + r) * g.N + n;
+                if (g.N % 4 == 0 && n < g.N)
+                    *reinterpret_cast<f32x4*>(to) = v;
+                else
+                    for (int i = 0; i < 4; ++i)
+                        if (n + i < g.N) to[i] = v[i];
+            }
+        } else if (n < g.N && whole) {
 #pragma unroll 1
             for (int r0 = lane / kLanes; r0 < 32; r0 += kAtOnce * kBatch) {
-                // a batch of rows, so that their reads are on their way together
-                float z[kBatch][4], res[kBatch][4];
+                // a batch of rows at once, the next batch's residual on its way
+                float z[kBatch][4];
+                Raw4<O> res[kBatch];
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
-                    const int r = r0 + u * kAtOnce;
-                    if (g.residual) get4(static_cast<const O*>(g.residual) + (size_t)min(top + r, g.M - 1) * g.N + n, res[u]);
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(turn + r * kPitch + lane % kLanes * 4);
+                    res[u] = ahead[u];
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(turn + (r0 + u * kAtOnce) * kPitch + lane % kLanes * 4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) z[u][i] = v[i];
                 }
+                if (g.residual) look_ahead(top + r0 + kAtOnce * kBatch);
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) {
                     const int m = top + r0 + u * kAtOnce;
@@ -435,9 +473,40 @@ __global__ __launch_bounds__(kThreads) void k_gemm(Gemm g) {
     });
 }
 
+// Adds the splits' sums in their order and finishes them: four outputs a thread.
+template <typename T, typename O>
+__global__ __launch_bounds__(kThreads) void k_finish(Gemm g) {
+    const int across = (g.N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int m = (int)(i / across), n = (int)(i % across) * 4;
+    if (m >= g.M) return;
+    float z[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool whole = four_at_once<T, O>(g);
+    for (int s = 0; s < g.splits; ++s) {
+        const float* p = g.part + ((size_t)s * g.M + m) * g.N + n;
+        if (whole) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] += v[j];
+        } else {
+            for (int j = 0; j < 4; ++j)
+                if (n + j < g.N) z[j] += p[j];
+        }
+    }
+    if (!whole) {
+        finish4<T, O>(g, m, n, z);
+        return;
+    }
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    Raw4<O> res = {};
+    if (g.bias) get4(static_cast<const T*>(g.bias) + n, bias);
+    if (g.residual) res = *reinterpret_cast<const Raw4<O>*>(static_cast<const O*>(g.residual) + (size_t)m * g.N + n);
+    finish4_whole<T, O>(g, m, n, bias, res, z);
+}
+
 // -------------------------------------------------------- product of few rows
-// M <= 16 MC: bound by reading W once.  A workgroup has 16 NR rows of W; its
-// four waves take every fourth piece of KS * 64 bytes of the rows, W and X
+// M <= 16: bound by reading W once.  A workgroup has 16 rows of W; its four
+// waves take every fourth piece of 256 bytes of the rows, W and X
 // straight into registers as operands of 16x16 instructions (lane l: row
 // l % 16, chunk l / 16), the next piece on its way while one is multiplied.
 // The waves' sums are added in LDS.
@@ -451,38 +520,28 @@ __device__ inline f32x4 mfma16(float, u32x4 a, u32x4 b, f32x4 c) {
     return c;
 }
 
-template <typename T, typename O, int MC, int NR, bool ALIGNED>
+template <typename T, typename O, bool ALIGNED>
 __global__ __launch_bounds__(kThreads) void k_few(Gemm g) {
-    constexpr int kElems = 16 / (int)sizeof(T), KS = MC * NR >= 8 ? 2 : 4, kPiece = KS * 4 * kElems;
-    constexpr int kPitch = 16 * NR + 4;
-    __shared__ float sums[4][16 * MC][kPitch];
+    constexpr int kElems = 16 / (int)sizeof(T), KS = 4, kPiece = KS * 4 * kElems, kPitch = 20;
+    __shared__ float sums[4][16][kPitch];
     const int t = threadIdx.x, lane = t & 63, w = t >> 6, r = lane & 15, c = lane >> 4;
-    const int n0 = blockIdx.x * 16 * NR;
-    const T *W[NR], *X[MC];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) W[i] = static_cast<const T*>(g.W) + min(n0 + i * 16 + r, g.N - 1) * g.ldw;
-#pragma unroll
-    for (int j = 0; j < MC; ++j) X[j] = static_cast<const T*>(g.X) + min(j * 16 + r, g.M - 1) * g.ldx;
+    const int n0 = blockIdx.x * 16;
+    const T* W = static_cast<const T*>(g.W) + min(n0 + r, g.N - 1) * g.ldw;
+    const T* X = static_cast<const T*>(g.X) + min(r, g.M - 1) * g.ldx;
     struct Piece {
-        u32x4 a[KS][NR], b[KS][MC];
+        u32x4 a[KS], b[KS];
     };
     auto load = [&](int p, Piece& q) {
         const bool full = ALIGNED && (p + 1) * kPiece <= g.K;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int k = p * kPiece + (s * 4 + c) * kElems;
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
-                q.a[s][i] = full ? *reinterpret_cast<const u32x4*>(W[i] + k) : chunk_of(W[i], k, g.K);
-#pragma unroll
-            for (int j = 0; j < MC; ++j) {
-                q.b[s][j] = (u32x4){0, 0, 0, 0};
-                if (j * 16 + r < g.M)
-                    q.b[s][j] = full ? *reinterpret_cast<const u32x4*>(X[j] + k) : chunk_of(X[j], k, g.K);
-            }
+            q.a[s] = full ? *reinterpret_cast<const u32x4*>(W + k) : chunk_of(W, k, g.K);
+            q.b[s] = (u32x4){0, 0, 0, 0};
+            if (r < g.M) q.b[s] = full ? *reinterpret_cast<const u32x4*>(X + k) : chunk_of(X, k, g.K);
         }
     };
-    f32x4 acc[NR][MC] = {};
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     const int pieces = (g.K + kPiece - 1) / kPiece;
     Piece q;
     if (w < pieces) load(w, q);
@@ -490,30 +549,24 @@ __global__ __launch_bounds__(kThreads) void k_few(Gemm g) {
         Piece next;
         if (p + 4 < pieces) load(p + 4, next);
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
-#pragma unroll
-                for (int j = 0; j < MC; ++j) acc[i][j] = mfma16(T(), q.a[s][i], q.b[s][j], acc[i][j]);
+        for (int s = 0; s < KS; ++s) acc = mfma16(T(), q.a[s], q.b[s], acc);
         q = next;
     }
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int j = 0; j < MC; ++j) *reinterpret_cast<f32x4*>(&sums[w][j * 16 + r][i * 16 + c * 4]) = acc[i][j];
+    *reinterpret_cast<f32x4*>(&sums[w][r][c * 4]) = acc;
     __syncthreads();
     const bool whole = four_at_once<T, O>(g);
-    for (int i = t; i < 16 * MC * 4 * NR; i += kThreads) {
-        const int m = i / (4 * NR), n = i % (4 * NR) * 4;
+    if (t < 64) {
+        const int m = t / 4, n = t % 4 * 4;
         f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][m][n]);
 #pragma unroll
         for (int k = 1; k < 4; ++k) v += *reinterpret_cast<const f32x4*>(&sums[k][m][n]);
         float z[4] = {v[0], v[1], v[2], v[3]};
-        if (m >= g.M || n0 + n >= g.N) continue;
+        if (m >= g.M || n0 + n >= g.N) return;
         if (whole) {
-            float bias[4] = {0.f, 0.f, 0.f, 0.f}, res[4];
+            float bias[4] = {0.f, 0.f, 0.f, 0.f};
+            Raw4<O> res = {};
             if (g.bias) get4(static_cast<const T*>(g.bias) + n0 + n, bias);
-            if (g.residual) get4(static_cast<const O*>(g.residual) + (size_t)m * g.N + n0 + n, res);
+            if (g.residual) res = *reinterpret_cast<const Raw4<O>*>(static_cast<const O*>(g.residual) + (size_t)m * g.N + n0 + n);
             finish4_whole<T, O>(g, m, n0 + n, bias, res, z);
         } else {
             finish4<T, O>(g, m, n0 + n, z);
@@ -665,65 +718,94 @@ inline bool ws_ok(const void* p, size_t bytes, size_t need) {
 }
 inline spec_status launched() { return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP; }
 
-template <typename T, typename O, int BM, int BN, int WM, int WN, int kRowBytes, int STAGES, bool DIRECT>
-void launch_tiles(Gemm g, hipStream_t st) {
-    const int tm = (g.M + BM - 1) / BM;
-    g.tiles_n = (g.N + BN - 1) / BN;
-    k_gemm<T, O, BM, BN, WM, WN, kRowBytes, STAGES, DIRECT><<<(unsigned)tm * (unsigned)g.tiles_n, kThreads, 0, st>>>(g);
+// ------------------------------------------------------------ choice of kernel
+// A rule on sizes alone.  Up to 16 rows are read against W in registers
+// (k_few), but from kWide columns on up to 64 rows take tiles of 32 or 64 rows
+// by 128 of W, which keep more of W on its way (us at N 128256, K 4096, bf16:
+// one row 155, k_few 199; 32 rows 169, 187 with temporal loads).  Else the
+// largest tile that still gives kEnough workgroups: 256 (4096 x 4096 x 8192
+// bf16: 219 us; 128: 259), 128 (1024 x 4096 x 4096: 34 us), 64; and where 64
+// leaves compute units idle, K is split over several workgroups a tile, of at
+// least four steps each, their fp32 sums added by one more launch, where the
+// steps saved outweigh that launch (split / not, us: 512 x 512 x 8192 bf16
+// 18.6 / 26.6, fp32 45.8 / 140.8; 192 x 4096 x 4096 bf16 19.8 / 15.8).
+constexpr int kWide = 16384, kEnough = 200, kSplitGroups = 512, kMaxSplits = 8, kSplitWorth = 50;
+enum Choice { kFew, kRows32, kRows64, kTile256, kTile128, kTile64 };
+inline long long tiles_of(long long M, long long N, int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); }
+inline Choice choose(long long M, long long N) {
+    if (M <= 16 && N < kWide) return kFew;
+    if (M <= 32 && N >= kWide) return kRows32;
+    if (M <= 64 && N >= kWide) return kRows64;
+    return tiles_of(M, N, 256) >= kEnough ? kTile256 : tiles_of(M, N, 128) >= kEnough ? kTile128 : kTile64;
 }
-template <typename T, typename O, int MC, int NR>
-void launch_few(const Gemm& g, bool aligned, hipStream_t st) {
-    const unsigned grid = (unsigned)((g.N + 16 * NR - 1) / (16 * NR));
-    if (aligned)
-        k_few<T, O, MC, NR, true><<<grid, kThreads, 0, st>>>(g);
-    else
-        k_few<T, O, MC, NR, false><<<grid, kThreads, 0, st>>>(g);
+inline int splits_of(spec_dtype d, long long M, long long N, long long K) {
+    if (choose(M, N) != kTile64) return 1;
+    const long long step = 128 / (long long)elem(d), steps = (K + step - 1) / step;
+    const long long want = kSplitGroups / tiles_of(M, N, 64);
+    long long s = want < steps / 4 ? want : steps / 4;
+    s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+    const long long per = (steps + s - 1) / s;
+    // the second launch costs some 4 us, a step 0.18 us in bf16 and 0.54 in fp32
+    if ((steps - per) * (d == SPEC_BF16 ? 1 : 3) < kSplitWorth) return 1;
+    return (int)((steps + per - 1) / per);  // no split without steps
 }
-template <typename T, typename O, int MC>
-void launch_few(const Gemm& g, bool aligned, hipStream_t st) {
-    if (g.N >= 64 * 512)
-        launch_few<T, O, MC, 4>(g, aligned, st);
-    else
-        launch_few<T, O, MC, 1>(g, aligned, st);
+inline size_t split_bytes(spec_dtype d, long long M, long long N, long long K) {
+    const int s = splits_of(d, M, N, K);
+    return s > 1 ? align_up((size_t)s * (size_t)(M * N) * 4, 256) : 0;
 }
 
+template <typename T, typename O, int BM, int BN, int WM, int WN, int kRowBytes, int STAGES, bool DIRECT>
+void launch_tiles(Gemm g, hipStream_t st) {
+    g.tiles_n = (g.N + BN - 1) / BN;
+    const unsigned grid = (unsigned)((g.M + BM - 1) / BM) * (unsigned)g.tiles_n * (unsigned)g.splits;
+    k_gemm<T, O, BM, BN, WM, WN, kRowBytes, STAGES, DIRECT><<<grid, kThreads, 0, st>>>(g);
+    if (g.splits > 1) {
+        const int64_t four = (int64_t)g.M * ((g.N + 3) / 4);
+        k_finish<T, O><<<(unsigned)((four + kThreads - 1) / kThreads), kThreads, 0, st>>>(g);
+    }
+}
 template <typename T, typename O>
-void launch_typed(const Gemm& g, hipStream_t st) {
+void launch_typed(Gemm g, spec_dtype d, hipStream_t st) {
     const uintptr_t a = (uintptr_t)g.X | (uintptr_t)g.W | (uintptr_t)(g.ldx * (int64_t)sizeof(T)) | (uintptr_t)(g.ldw * (int64_t)sizeof(T));
-    auto tiles = [&](int b) { return (long long)((g.M + b - 1) / b) * ((g.N + b - 1) / b); };
-    if (g.M <= 16)
-        launch_few<T, O, 1>(g, a % 16 == 0, st);
-    else if (g.M <= 32 && a % 16 == 0 && g.N >= 16384)
-        launch_tiles<T, O, 32, 128, 32, 32, 128, 4, true>(g, st);
-    else if (g.M <= 64 && g.M > 32 && a % 16 == 0 && g.N >= 16384)
-        launch_tiles<T, O, 64, 128, 64, 32, 128, 3, true>(g, st);
-    else if (g.M <= 32)
-        launch_few<T, O, 2>(g, a % 16 == 0, st);
-    else if (g.M <= 64)
-        launch_few<T, O, 4>(g, a % 16 == 0, st);
-    else if (a % 16 != 0)
+    const bool direct = a % 16 == 0;
+    const Choice c = choose(g.M, g.N);
+    g.splits = 1;
+    if (c == kFew) {
+        const unsigned grid = (unsigned)((g.N + 15) / 16);
+        if (direct)
+            k_few<T, O, true><<<grid, kThreads, 0, st>>>(g);
+        else
+            k_few<T, O, false><<<grid, kThreads, 0, st>>>(g);
+    } else if (!direct) {  // rows that start anywhere: through registers
+        g.splits = splits_of(d, g.M, g.N, g.K);
         launch_tiles<T, O, 64, 64, 32, 32, 128, 2, false>(g, st);
-    else if (tiles(256) >= 200)
+    } else if (c == kRows32) {
+        launch_tiles<T, O, 32, 128, 32, 32, 128, 4, true>(g, st);
+    } else if (c == kRows64) {
+        launch_tiles<T, O, 64, 128, 64, 32, 128, 3, true>(g, st);
+    } else if (c == kTile256) {
         launch_tiles<T, O, 256, 256, 128, 128, 128, 2, true>(g, st);
-    else if (tiles(128) >= 200)
+    } else if (c == kTile128) {
         launch_tiles<T, O, 128, 128, 64, 64, 128, 4, true>(g, st);
-    else
+    } else {
+        g.splits = splits_of(d, g.M, g.N, g.K);
         launch_tiles<T, O, 64, 64, 32, 32, 128, 4, true>(g, st);
+    }
 }
 void launch_gemm(const Gemm& g, spec_dtype d, spec_dtype o, hipStream_t st) {
     if (d == SPEC_F32)
-        launch_typed<float, float>(g, st);
+        launch_typed<float, float>(g, d, st);
     else if (o == SPEC_F32)
-        launch_typed<bf16, float>(g, st);
+        launch_typed<bf16, float>(g, d, st);
     else
-        launch_typed<bf16, bf16>(g, st);
+        launch_typed<bf16, bf16>(g, d, st);
 }
 
 // The gradients' workspace: dz, dz turned, x and W turned, rows padded to whole
-// chunks, and the bias gradient's parts.
+// chunks, the bias gradient's parts, and the sums of a split product.
 struct GradLayout {
     int64_t np, mp;  // padded N and M
-    size_t dz, dzt, xt, wt, part, total;
+    size_t dz, dzt, xt, wt, part, sums, total;
 };
 inline GradLayout grad_layout(spec_dtype d, long long M, long long N, long long K) {
     const long long e = (long long)elem(d), c = 16 / e;
@@ -735,7 +817,9 @@ inline GradLayout grad_layout(spec_dtype d, long long M, long long N, long long 
     l.xt = align_up(l.dzt + (size_t)(N * l.mp * e), 256);
     l.wt = align_up(l.xt + (size_t)(K * l.mp * e), 256);
     l.part = align_up(l.wt + (size_t)(K * l.np * e), 256);
-    l.total = align_up(l.part + (size_t)((M + 63) / 64 * N * 4), 256);
+    l.sums = align_up(l.part + (size_t)((M + 63) / 64 * N * 4), 256);  // of K's splits: one product at a time
+    const size_t a = split_bytes(d, M, K, l.np), b = split_bytes(d, N, K, l.mp);
+    l.total = l.sums + (a > b ? a : b);
     return l;
 }
 
@@ -760,7 +844,8 @@ void launch_slopes(Slopes& a, spec_dtype in, spec_dtype d, hipStream_t st) {
 
 extern "C" size_t spec_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K) {
     if (!types_ok(dtype, SPEC_F32) || !sizes_ok(M, N, K)) return 0;
-    return 256;
+    const size_t n = split_bytes(dtype, M, N, K);
+    return n ? n : 256;
 }
 
 extern "C" spec_status spec_linear(const void* x, const void* weight, const void* bias, const void* residual,
@@ -770,7 +855,7 @@ extern "C" spec_status spec_linear(const void* x, const void* weight, const void
     if (!types_ok(dtype, out_dtype)) return SPEC_EDTYPE;
     if (!sizes_ok(M, N, K) || !act_ok(activation) || !x || !weight || !out) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_linear_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
-    const Gemm g{x, weight, K, K, M, N, K, bias, residual, activation, out, out_preact, 0};
+    const Gemm g{x, weight, K, K, M, N, K, bias, residual, activation, out, out_preact, 0, 1, static_cast<float*>(workspace)};
     launch_gemm(g, dtype, out_dtype, static_cast<hipStream_t>(stream));
     return launched();
 }
@@ -796,6 +881,7 @@ extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const
     // without an activation dy is dz where it has the operands' type and
     // aligned rows
     const bool as_is = !z && dtype == out_dtype && lay.np == N && (uintptr_t)grad_out % 16 == 0;
+    float* sums = reinterpret_cast<float*>(ws + lay.sums);
     Slopes s{};
     s.job[0] = {grad_out, z, activation, M, N, grad_x && !as_is ? ws + lay.dz : nullptr,
                 grad_weight ? ws + lay.dzt : nullptr, lay.np, lay.mp,
@@ -812,10 +898,10 @@ extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const
             k_bias_sum<bf16><<<(N + 63) / 64, 64 * kSumWaves, 0, st>>>(part, parts, N, (bf16*)grad_bias);
     }
     if (grad_x)
-        launch_gemm({as_is ? grad_out : ws + lay.dz, ws + lay.wt, lay.np, lay.np, M, K, (int)lay.np, nullptr, nullptr, 0, grad_x, nullptr, 0},
+        launch_gemm({as_is ? grad_out : ws + lay.dz, ws + lay.wt, lay.np, lay.np, M, K, (int)lay.np, nullptr, nullptr, 0, grad_x, nullptr, 0, 1, sums},
                     dtype, dtype, st);
     if (grad_weight)
-        launch_gemm({ws + lay.dzt, ws + lay.xt, lay.mp, lay.mp, N, K, (int)lay.mp, nullptr, nullptr, 0, grad_weight, nullptr, 0},
+        launch_gemm({ws + lay.dzt, ws + lay.xt, lay.mp, lay.mp, N, K, (int)lay.mp, nullptr, nullptr, 0, grad_weight, nullptr, 0, 1, sums},
                     dtype, dtype, st);
     return launched();
 }
