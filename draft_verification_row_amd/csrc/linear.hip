@@ -577,7 +577,7 @@ __global__ __launch_bounds__(kThreads) void k_few(Gemm g) {
 // ---------------------------------------------------------- gradients' inputs
 // dz = dy act'(z) to dz [M][ld] and, turned, to dzt [N][ldt], rounded, zero up
 // to the rows' ends; sums of 64 rows' unrounded dz to part [M/64][N].  Each of
-// the three is optional.  The same kernel turns a matrix (dy alone).  Bound by
+// the three is optional.  The same kernel turns or pads a matrix (dy alone).  Bound by
 // memory: a thread reads and writes eight neighbouring elements at once
 // (VECTOR: N a multiple of 8 and 16-byte aligned inputs; ld and ldt are whole
 // 16-byte chunks always), the turning goes through LDS.
@@ -604,6 +604,13 @@ __device__ inline void get8(const I* p, int left, float (&v)[8]) {
         get4(p + 4, b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = a[i], v[i + 4] = b[i];
+    } else if (left >= 8) {  // at any alignment
+        struct Any {
+            I v[8];
+        } __attribute__((packed, aligned(sizeof(I))));
+        const Any q = *reinterpret_cast<const Any*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f(q.v[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f(p[i]) : 0.f;
@@ -754,6 +761,23 @@ inline size_t split_bytes(spec_dtype d, long long M, long long N, long long K) {
     return s > 1 ? align_up((size_t)s * (size_t)(M * N) * 4, 256) : 0;
 }
 
+// A K that is no whole number of chunks leaves rows that cannot be loaded
+// directly.  For the larger tiles both operands are copied to padded rows
+// first, which costs their bytes once; the smaller ones load through registers
+// (copied / not, us: 4096 x 4096 x 4095 bf16 172 / 384, fp32 1005 / 1220,
+// 1500 x 2000 x 777 bf16 20.2 / 20.7).
+inline bool packs(spec_dtype d, long long M, long long N, long long K) {
+    const Choice c = choose(M, N);
+    return K * (long long)elem(d) % 16 != 0 && (c == kTile256 || c == kTile128);
+}
+inline long long padded(spec_dtype d, long long n) {
+    const long long c = 16 / (long long)elem(d);
+    return (n + c - 1) / c * c;
+}
+inline size_t packed_x_bytes(spec_dtype d, long long M, long long K) {
+    return align_up((size_t)(M * padded(d, K)) * elem(d), 256);
+}
+
 template <typename T, typename O, int BM, int BN, int WM, int WN, int kRowBytes, int STAGES, bool DIRECT>
 void launch_tiles(Gemm g, hipStream_t st) {
     g.tiles_n = (g.N + BN - 1) / BN;
@@ -808,10 +832,10 @@ struct GradLayout {
     size_t dz, dzt, xt, wt, part, sums, total;
 };
 inline GradLayout grad_layout(spec_dtype d, long long M, long long N, long long K) {
-    const long long e = (long long)elem(d), c = 16 / e;
+    const long long e = (long long)elem(d);
     GradLayout l;
-    l.np = (N + c - 1) / c * c;
-    l.mp = (M + c - 1) / c * c;
+    l.np = padded(d, N);
+    l.mp = padded(d, M);
     l.dz = 0;
     l.dzt = align_up(l.dz + (size_t)(M * l.np * e), 256);
     l.xt = align_up(l.dzt + (size_t)(N * l.mp * e), 256);
@@ -844,6 +868,7 @@ void launch_slopes(Slopes& a, spec_dtype in, spec_dtype d, hipStream_t st) {
 
 extern "C" size_t spec_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K) {
     if (!types_ok(dtype, SPEC_F32) || !sizes_ok(M, N, K)) return 0;
+    if (packs(dtype, M, N, K)) return packed_x_bytes(dtype, M, K) + packed_x_bytes(dtype, N, K);
     const size_t n = split_bytes(dtype, M, N, K);
     return n ? n : 256;
 }
@@ -855,7 +880,19 @@ extern "C" spec_status spec_linear(const void* x, const void* weight, const void
     if (!types_ok(dtype, out_dtype)) return SPEC_EDTYPE;
     if (!sizes_ok(M, N, K) || !act_ok(activation) || !x || !weight || !out) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_linear_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
-    const Gemm g{x, weight, K, K, M, N, K, bias, residual, activation, out, out_preact, 0, 1, static_cast<float*>(workspace)};
+    Gemm g{x, weight, K, K, M, N, K, bias, residual, activation, out, out_preact, 0, 1, static_cast<float*>(workspace)};
+    if (packs(dtype, M, N, K)) {
+        char *xp = static_cast<char*>(workspace), *wp = xp + packed_x_bytes(dtype, M, K);
+        const int64_t ld = padded(dtype, K);
+        Slopes s{};
+        s.job[1] = {weight, nullptr, 0, N, K, wp, nullptr, ld, 0, nullptr, false};
+        s.job[2] = {x, nullptr, 0, M, K, xp, nullptr, ld, 0, nullptr, false};
+        launch_slopes(s, dtype, dtype, static_cast<hipStream_t>(stream));
+        g.X = xp;
+        g.W = wp;
+        g.ldx = g.ldw = ld;
+        g.K = (int)ld;  // the padding is zero
+    }
     launch_gemm(g, dtype, out_dtype, static_cast<hipStream_t>(stream));
     return launched();
 }

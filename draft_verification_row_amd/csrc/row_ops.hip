@@ -829,6 +829,7 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     if (!rows_ok(dtype, rows, V) || top_n < 0 || top_n > SPEC_MAX_TOP) return SPEC_EINVAL;
     if (!logits || !tokens || !out_logprob || !out_entropy || !out_status) return SPEC_EINVAL;
     if (top_n > 0 && (!out_top_tokens || !out_top_logprob)) return SPEC_EINVAL;
+    if ((uintptr_t)out_stats % 16) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_logprobs_workspace_bytes(dtype, rows, V, top_n))) return SPEC_EWORKSPACE;
     const Split s = split_of(dtype, rows, V);
     char* ws = static_cast<char*>(workspace);
@@ -850,6 +851,7 @@ extern "C" spec_status spec_token_logprobs_grad(const void* logits, spec_dtype d
                                                 void* stream) {
     if (!dtype_ok(dtype)) return SPEC_EDTYPE;
     if (!rows_ok(dtype, rows, V) || !logits || !tokens || !stats || !out_grad) return SPEC_EINVAL;
+    if ((uintptr_t)stats % 16) return SPEC_EINVAL;
     const int tiles = tiles_of(dtype, V);
     const LpGradArgs a{logits, tokens, stats, grad_logprob, grad_entropy, rows, V, tiles, out_grad};
     const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -876,6 +878,7 @@ extern "C" spec_status spec_draft_kl(const void* target_logits, const void* draf
                                      float* out_stats, void* workspace, size_t workspace_bytes, void* stream) {
     if (!dtype_ok(dtype)) return SPEC_EDTYPE;
     if (!kl_ok(dtype, B, K, target_rows, V) || !target_logits || !draft_logits || !out_kl) return SPEC_EINVAL;
+    if ((uintptr_t)out_stats % 16) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_draft_kl_workspace_bytes(dtype, B, K, V))) return SPEC_EWORKSPACE;
     const Split s = split_of(dtype, (long long)B * K, V);
     char* ws = static_cast<char*>(workspace);
@@ -897,6 +900,7 @@ extern "C" spec_status spec_draft_kl_grad(const void* target_logits, const void*
     if (!dtype_ok(dtype)) return SPEC_EDTYPE;
     if (!kl_ok(dtype, B, K, target_rows, V) || !target_logits || !draft_logits || !stats || !grad_kl || !out_grad)
         return SPEC_EINVAL;
+    if ((uintptr_t)stats % 16) return SPEC_EINVAL;
     const int tiles = tiles_of(dtype, V);
     const KlArgs a{target_logits, draft_logits, mask, K, target_rows, V, tiles, nullptr, const_cast<float*>(stats), grad_kl, out_grad, 1, 0, nullptr, nullptr};
     const hipStream_t st = static_cast<hipStream_t>(stream);

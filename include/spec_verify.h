@@ -512,7 +512,8 @@ spec_status spec_verify_exact_noalloc(const void *target_logits, const void *dra
  *                     (ignored where top_n = 0; top_n <= SPEC_MAX_TOP)
  *   out_status        [rows] int32: 0, or 1 for a token outside [-1, V): the
  *                     row is then treated as padded
- *   out_stats         [rows][4] float, or NULL: what the gradient needs
+ *   out_stats         [rows][4] float, 16-byte aligned, or NULL: what the
+ *                     gradient needs
  */
 #define SPEC_MAX_TOP 32
 size_t spec_logprobs_workspace_bytes(spec_dtype dtype, int rows, int V, int top_n);
@@ -541,7 +542,8 @@ spec_status spec_token_logprobs_grad(const void *logits, spec_dtype dtype, const
  *
  *   target_logits [B][target_rows][V], draft_logits [B][K][V], same dtype
  *   mask          [B][K] bytes, or NULL (every row counts)
- *   out_kl        [B][K] float; out_stats [B][K][4] float, or NULL
+ *   out_kl        [B][K] float; out_stats [B][K][4] float, 16-byte aligned,
+ *                 or NULL
  * The gradient is to the draft's logits alone: grad_kl (q - p), in their
  * dtype; 0 also where the draft's row is -inf alone.
  */

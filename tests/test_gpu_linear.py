@@ -135,7 +135,8 @@ def test_linear_alignment(M, N, K, dtype, off):
     check(M, N, K, dtype, None, "silu", True, True, off=off)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 128256, 256), (32, 32000, 512), (700, 4096, 2048), (2048, 2304, 1024), (4096, 512, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 128256, 256), (32, 32000, 512), (700, 4096, 2048), (2048, 2304, 1024), (4096, 512, 512),
+                                   (1500, 2000, 777), (4000, 4100, 131)])
 def test_linear_larger(M, N, K):
     check(M, N, K, "bf16", "bf16", "silu", True, True)
 
@@ -144,6 +145,14 @@ def test_linear_long_sums():
     check(3, 40, 100000, "bf16", "f32", "none", backward=True)
     check(100000, 24, 16, "bf16", "bf16", "gelu", bias=True)
     check(70, 90, 50001, "f32", "f32", "none", backward=False)
+
+
+def test_linear_few_tiles_split():
+    """Few outputs of a long sum: K over several workgroups."""
+    for M, N, K in ((100, 300, 4000), (70, 129, 5001), (65, 64, 16384)):
+        check(M, N, K, "bf16", "bf16", "gelu", True, True)
+        check(M, N, K, "f32", "f32", "silu", True, True)
+    check(300, 6, 9000, "bf16", "f32", "relu", True, False)
 
 
 def test_linear_special_values():

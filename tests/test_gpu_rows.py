@@ -191,6 +191,21 @@ def test_logprobs_masks(V, dtype):
     assert r.logprob[5] == -math.inf
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lanes", [(31, 7, 7, 7), (31, 31, 31, 31), (64, 0, 0, 0), (3, 0, 1, 9), (0, 0, 0, 1)])
+def test_logprobs_uneven_masks(lanes, dtype):
+    """Finite logits under a few of each wave's lanes only, so that the waves'
+    bounds are loose and a tile may have more candidates than its list holds."""
+    dt = DT[dtype]
+    vec = 8 if dtype == "bf16" else 4
+    V = 40000
+    t = torch.arange(V, device="cuda") // vec % 256
+    keep = torch.tensor(lanes, device="cuda")[t // 64] > t % 64
+    X = rows_of(3, V, dt, seed=7).masked_fill(~keep, -math.inf)
+    X[1] = torch.where(keep, 1.0, -math.inf).to(dt)   # all of them tied
+    check(X.contiguous(), tokens_of(3, V, 7), top_n=32)
+
+
 @pytest.mark.parametrize("V", [100, 20001])
 def test_logprobs_padded_rows_are_not_read(V):
     """Token -1: NaN and +inf logits behind it do not matter; a token outside

@@ -43,7 +43,7 @@ def test_logprobs_argument_errors(lib):
     assert f(dt=2) == EDTYPE and f(dt=-1) == EDTYPE
     for bad in (dict(rows=0), dict(rows=-1), dict(V=0), dict(V=262145), dict(top=-1), dict(top=33), dict(X=None),
                 dict(tok=None), dict(lp=None), dict(ent=None), dict(tt=None), dict(tl=None), dict(st=None),
-                dict(rows=1 << 24)):
+                dict(rows=1 << 24), dict(stats=P + 4)):
         assert f(**bad) == EINVAL, bad
     assert f(ws=None) == EWORKSPACE and f(ws=WS + 8) == EWORKSPACE and f(wsb=0) == EWORKSPACE
     g = lib.spec_token_logprobs_grad
@@ -52,6 +52,7 @@ def test_logprobs_argument_errors(lib):
     assert g(P, 1, None, P, P, P, 4, 100, P, None) == EINVAL
     assert g(P, 1, P, None, P, P, 4, 100, P, None) == EINVAL
     assert g(P, 1, P, P, P, P, 0, 100, P, None) == EINVAL
+    assert g(P, 1, P, P + 8, P, P, 4, 100, P, None) == EINVAL
     assert g(P, 1, P, P, P, P, 4, 100, None, None) == EINVAL
 
 
@@ -65,7 +66,7 @@ def test_kl_argument_errors(lib):
 
     assert f(dt=7) == EDTYPE
     for bad in (dict(T=None), dict(D=None), dict(kl=None), dict(B=0), dict(K=0), dict(Kt=2), dict(V=0),
-                dict(V=262145)):
+                dict(V=262145), dict(stats=P + 4)):
         assert f(**bad) == EINVAL, bad
     assert f(ws=None) == EWORKSPACE and f(wsb=0) == EWORKSPACE and f(ws=WS + 16) == EWORKSPACE
     g = lib.spec_draft_kl_grad
