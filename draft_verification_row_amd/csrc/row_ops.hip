@@ -395,6 +395,11 @@ __device__ inline bool last_to_come(uint32_t* counter, int parts) {
 // logits above the last one kept (their indices are higher, so a tie loses).
 // U: blocks per thread and tile.  The next tile is loaded while one is worked
 // on.
+// Bound by reading where there are many rows: 2048 rows of 151936 bf16 take
+// 110 us (5.7 TB/s), 160 us with 20 alternatives, whose scan for candidates
+// costs about as many instructions as the statistics.  144 rows of 128256 take
+// 14 us (2.6 TB/s), 25 us with 20; six rows 7.5 and 12.5 us: there it is the
+// launch, the join and the fold, one after the other.
 template <typename T, bool TOP, int U>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
     constexpr int kVec = Row<T>::kVec;
@@ -534,7 +539,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 int above = 0;
 #pragma unroll 8
-                for (int j = 0; j < 64; ++j) above += best.key[j] > head;
+                for (int j = 0; j < kMaxParts; ++j) above += best.key[j] > head;
                 uint64_t bound = above == n - 1 ? head : 0;
                 bound = tail > bound ? tail : bound;
 #pragma unroll
@@ -572,7 +577,9 @@ struct LpGradArgs {
     void* grad;
 };
 
-// One workgroup per tile of a row: reads its logits and writes their gradient.
+// One workgroup per tile of a row: reads its logits and writes their gradient,
+// bound by both: 192 us for 2048 rows of 151936 bf16, a tenth of them padded
+// and only written (6.2 TB/s).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
     constexpr int kVec = Row<T>::kVec;
@@ -624,6 +631,8 @@ struct KlArgs {
 };
 
 // Split over workgroups like k_logprobs.  Blocks follow the target's row.
+// Bound by reading both rows and, close behind, by two exponentials a token:
+// 205 us for 1844 rows of 128255 bf16 (4.6 TB/s), 23 us for 128 of 128256.
 template <typename T, bool ALIGNED>
 __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, Pair& st) {
     constexpr int kVec = Row<T>::kVec;
@@ -710,7 +719,8 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
     }
 }
 
-// One workgroup per tile of a draft row: reads both rows, writes the gradient.
+// One workgroup per tile of a draft row: reads both rows, writes the gradient:
+// 247 us for 2048 rows of 128255 bf16, a tenth of them masked (6.0 TB/s).
 template <typename T, bool ALIGNED>
 __device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Beside<T>& P, T* out, bool whole, int tile, const float4& s, float g) {
     constexpr int kVec = Row<T>::kVec;

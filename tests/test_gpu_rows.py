@@ -206,6 +206,17 @@ def test_logprobs_uneven_masks(lanes, dtype):
     check(X.contiguous(), tokens_of(3, V, 7), top_n=32)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [2, 700])
+def test_logprobs_rising_rows(rows, dtype):
+    """Logits that rise along the row, in steps and strictly: every tile has
+    better tokens than the last."""
+    V = 30000
+    x = torch.arange(V, device="cuda") / 500
+    X = torch.stack([x, x.floor(), -x, x % 17] * ((rows + 3) // 4))[:rows].to(DT[dtype]).contiguous()
+    check(X, tokens_of(rows, V, 3), top_n=32, backward=False)
+
+
 @pytest.mark.parametrize("V", [100, 20001])
 def test_logprobs_padded_rows_are_not_read(V):
     """Token -1: NaN and +inf logits behind it do not matter; a token outside
