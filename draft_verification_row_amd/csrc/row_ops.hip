@@ -371,7 +371,7 @@ __device__ inline float high(uint64_t w) { return __uint_as_float((uint32_t)(w >
 // the others published before is then visible, since published words are
 // written and read with agent-scope atomics, past the XCDs' caches, and have
 // arrived before the counter is raised (a release fence would write back and
-// invalidate the whole XCD's cache: 47 us instead of 17 for the divergence of
+// invalidate the whole XCD's cache: 47 us instead of 27 for the divergence of
 // 160 rows of 128256).  The last one leaves the counter at zero.
 __device__ inline bool last_to_come(uint32_t* counter, int parts) {
     __shared__ int last;
