@@ -594,7 +594,8 @@ struct Slope {
     int act, M, N;
     void *dz, *dzt;
     int64_t ld, ldt;
-    float* part;
+    float* part;  // or, where there is one part,
+    void* sum;    // the bias gradient itself
     bool vector;
 };
 // Up to three of them in one launch: dz, then W and x turned (jobs 1 and 2 are
@@ -672,11 +673,15 @@ __device__ inline void slope_block(const Slope& a, unsigned block, float (&tile)
             for (int i = 0; i < 8; ++i) v[i] = tile[c + i][r];
             if (n < a.N && m < a.ldt) put8(static_cast<T*>(a.dzt) + (size_t)n * a.ldt + m, a.ldt - m, v);
         }
-    if (a.part && t < 64 && n0 + t < a.N) {
+    if ((a.part || a.sum) && t < 64 && n0 + t < a.N) {
         float s[4] = {};
 #pragma unroll
         for (int r = 0; r < 64; ++r) s[r % 4] += tile[r][t];
-        a.part[(size_t)row * a.N + n0 + t] = (s[0] + s[1]) + (s[2] + s[3]);
+        const float all = (s[0] + s[1]) + (s[2] + s[3]);
+        if (a.sum)
+            put(static_cast<T*>(a.sum) + n0 + t, all);
+        else
+            a.part[(size_t)row * a.N + n0 + t] = all;
     }
 }
 
@@ -865,7 +870,7 @@ void launch_slopes(Slopes& a, spec_dtype in, spec_dtype d, hipStream_t st) {
     for (int i = 0; i < 3; ++i) {
         Slope& s = a.job[i];
         s.vector = s.N % 8 == 0 && ((uintptr_t)s.dy | (uintptr_t)s.preact) % 16 == 0;
-        if (s.dz || s.dzt || s.part) blocks += (unsigned)((s.N + 63) / 64) * (unsigned)((s.M + 63) / 64);
+        if (s.dz || s.dzt || s.part || s.sum) blocks += (unsigned)((s.N + 63) / 64) * (unsigned)((s.M + 63) / 64);
         a.end[i] = blocks;
     }
     if (blocks == 0) return;
@@ -898,8 +903,8 @@ extern "C" spec_status spec_linear(const void* x, const void* weight, const void
         char *xp = static_cast<char*>(workspace), *wp = xp + packed_x_bytes(dtype, M, K);
         const int64_t ld = padded(dtype, K);
         Slopes s{};
-        s.job[1] = {weight, nullptr, 0, N, K, wp, nullptr, ld, 0, nullptr, false};
-        s.job[2] = {x, nullptr, 0, M, K, xp, nullptr, ld, 0, nullptr, false};
+        s.job[1] = {weight, nullptr, 0, N, K, wp, nullptr, ld, 0, nullptr, nullptr, false};
+        s.job[2] = {x, nullptr, 0, M, K, xp, nullptr, ld, 0, nullptr, nullptr, false};
         launch_slopes(s, dtype, dtype, static_cast<hipStream_t>(stream));
         g.X = xp;
         g.W = wp;
@@ -935,11 +940,12 @@ extern "C" spec_status spec_linear_grad(const void* x, const void* weight, const
     Slopes s{};
     s.job[0] = {grad_out, z, activation, M, N, grad_x && !as_is ? ws + lay.dz : nullptr,
                 grad_weight ? ws + lay.dzt : nullptr, lay.np, lay.mp,
-                grad_bias ? reinterpret_cast<float*>(ws + lay.part) : nullptr, false};
-    if (grad_x) s.job[1] = {weight, nullptr, 0, N, K, nullptr, ws + lay.wt, 0, lay.np, nullptr, false};
-    if (grad_weight) s.job[2] = {x, nullptr, 0, M, K, nullptr, ws + lay.xt, 0, lay.mp, nullptr, false};
+                grad_bias && M > 64 ? reinterpret_cast<float*>(ws + lay.part) : nullptr,
+                grad_bias && M <= 64 ? grad_bias : nullptr, false};
+    if (grad_x) s.job[1] = {weight, nullptr, 0, N, K, nullptr, ws + lay.wt, 0, lay.np, nullptr, nullptr, false};
+    if (grad_weight) s.job[2] = {x, nullptr, 0, M, K, nullptr, ws + lay.xt, 0, lay.mp, nullptr, nullptr, false};
     launch_slopes(s, out_dtype, dtype, st);
-    if (grad_bias) {
+    if (s.job[0].part) {
         const float* part = reinterpret_cast<const float*>(ws + lay.part);
         const int parts = (M + 63) / 64;
         if (dtype == SPEC_F32)

@@ -58,7 +58,9 @@ struct Row {
         rsrc = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(a0), (short)0, nvec * 16, kRsrcWord3);
     }
     __device__ int first(int i) const { return i * kVec - shift; }  // element of block i's place 0
-    __device__ u32x4 raw(int i) const { return __builtin_amdgcn_raw_buffer_load_b128(rsrc, i * 16, 0, 0); }
+    // ONCE: a non-temporal load, for rows that the caches cannot keep
+    template <bool ONCE>
+    __device__ u32x4 raw(int i) const { return __builtin_amdgcn_raw_buffer_load_b128(rsrc, i * 16, 0, ONCE ? 2 : 0); }
     // the elements e .. e + kVec - 1, widened; -inf outside the row
     __device__ void unpack(u32x4 q, int e, float (&v)[kVec]) const {
         if constexpr (sizeof(T) == 2) {
@@ -96,12 +98,12 @@ struct Beside {
         bytes = by & 3;
     }
     __device__ bool aligned() const { return (dwords | bytes) == 0; }
-    template <bool ALIGNED>
+    template <bool ONCE, bool ALIGNED>
     __device__ u32x4 from(int i) const {
         // block -1 lies past the descriptor's size like any other outside block
-        const u32x4 a = r.raw(i + block);
+        const u32x4 a = r.template raw<ONCE && ALIGNED>(i + block);
         if constexpr (ALIGNED) return a;
-        const u32x4 b = r.raw(i + block + 1);
+        const u32x4 b = r.template raw<false>(i + block + 1);
         u32x4 q;
         uint32_t x[5];
 #pragma unroll
@@ -400,7 +402,7 @@ __device__ inline bool last_to_come(uint32_t* counter, int parts) {
 // costs about as many instructions as the statistics.  144 rows of 128256 take
 // 14 us (2.6 TB/s), 25 us with 20; six rows 7.5 and 12.5 us: there it is the
 // launch, the join and the fold, one after the other.
-template <typename T, bool TOP, int U>
+template <typename T, bool TOP, int U, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
     constexpr int kVec = Row<T>::kVec;
     const int r = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x, w = t >> 6;
@@ -427,7 +429,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
     int count = 0;
     u32x4 q[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) q[u] = R.raw(begin + u * kThreads + t);
+    for (int u = 0; u < U; ++u) q[u] = R.template raw<ONCE>(begin + u * kThreads + t);
     for (int base = begin; base < R.nvec; base += U * kThreads) {
         float v[U][kVec], m = -INFINITY;
         int e[U];
@@ -435,7 +437,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
         for (int u = 0; u < U; ++u) {
             e[u] = R.first(base + u * kThreads + t);
             R.unpack(q[u], e[u], v[u]);
-            q[u] = R.raw(base + (U + u) * kThreads + t);
+            q[u] = R.template raw<ONCE>(base + (U + u) * kThreads + t);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -580,7 +582,7 @@ struct LpGradArgs {
 // One workgroup per tile of a row: reads its logits and writes their gradient,
 // bound by both: 192 us for 2048 rows of 151936 bf16, a tenth of them padded
 // and only written (6.2 TB/s).
-template <typename T>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
     constexpr int kVec = Row<T>::kVec;
     const int r = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles, t = threadIdx.x;
@@ -600,7 +602,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
         if (i >= R.nvec) break;
         float v[kVec];
         if (live) {
-            R.unpack(R.raw(i), R.first(i), v);
+            R.unpack(R.template raw<ONCE>(i), R.first(i), v);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float lp = (v[j] - ref) - ls, p = exp2_(lp * kLog2e);
@@ -633,15 +635,15 @@ struct KlArgs {
 // Split over workgroups like k_logprobs.  Blocks follow the target's row.
 // Bound by reading both rows and, close behind, by two exponentials a token:
 // 205 us for 1844 rows of 128255 bf16 (4.6 TB/s), 23 us for 128 of 128256.
-template <typename T, bool ALIGNED>
+template <typename T, bool ONCE, bool ALIGNED>
 __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, Pair& st) {
     constexpr int kVec = Row<T>::kVec;
     constexpr int kSteps = kUnroll / 2;  // two rows: as many loads in flight
     u32x4 x[kSteps], y[kSteps];
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-        x[u] = P.raw(begin + u * kThreads + (int)threadIdx.x);
-        y[u] = Q.template from<ALIGNED>(begin + u * kThreads + (int)threadIdx.x);
+        x[u] = P.template raw<ONCE>(begin + u * kThreads + (int)threadIdx.x);
+        y[u] = Q.template from<ONCE, ALIGNED>(begin + u * kThreads + (int)threadIdx.x);
     }
     for (int base = begin; base < P.nvec; base += kSteps * kThreads) {
         float p[kSteps][kVec], q[kSteps][kVec], m = -INFINITY, n = -INFINITY;
@@ -650,8 +652,8 @@ __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, 
             const int i = base + u * kThreads + (int)threadIdx.x, e = P.first(i);
             P.unpack(x[u], e, p[u]);
             P.unpack(y[u], e, q[u]);
-            x[u] = P.raw(i + kSteps * kThreads);
-            y[u] = Q.template from<ALIGNED>(i + kSteps * kThreads);
+            x[u] = P.template raw<ONCE>(i + kSteps * kThreads);
+            y[u] = Q.template from<ONCE, ALIGNED>(i + kSteps * kThreads);
         }
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
@@ -675,7 +677,7 @@ __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, 
     }
 }
 
-template <typename T>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
     const int r = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x;
     if (a.mask && !a.mask[r]) {
@@ -690,9 +692,9 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
     const Beside<T> Q(static_cast<const T*>(a.draft) + (size_t)r * a.V, a.V, P);
     Pair st{-INFINITY, 0.f, -INFINITY, 0.f, 0.f};
     if (Q.aligned())
-        kl_sweep<T, true>(P, Q, begin, st);
+        kl_sweep<T, ONCE, true>(P, Q, begin, st);
     else
-        kl_sweep<T, false>(P, Q, begin, st);
+        kl_sweep<T, ONCE, false>(P, Q, begin, st);
     st = join_group(st);
     if (a.parts > 1) {
         uint64_t* rec = a.records + ((size_t)r * a.parts + part) * 3;
@@ -721,15 +723,15 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
 
 // One workgroup per tile of a draft row: reads both rows, writes the gradient:
 // 247 us for 2048 rows of 128255 bf16, a tenth of them masked (6.0 TB/s).
-template <typename T, bool ALIGNED>
+template <typename T, bool ONCE, bool ALIGNED>
 __device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Beside<T>& P, T* out, bool whole, int tile, const float4& s, float g) {
     constexpr int kVec = Row<T>::kVec;
     u32x4 x[kUnroll], y[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const int i = tile * kTileVecs + u * kThreads + (int)threadIdx.x;
-        x[u] = D.raw(i);
-        y[u] = P.template from<ALIGNED>(i);
+        x[u] = D.template raw<ONCE>(i);
+        y[u] = P.template from<ONCE, ALIGNED>(i);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -745,7 +747,7 @@ __device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Besi
     }
 }
 
-template <typename T>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_draft_kl_grad(KlArgs a) {
     constexpr int kVec = Row<T>::kVec;
     const int r = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles, t = threadIdx.x;
@@ -767,9 +769,9 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl_grad(KlArgs a) {
     const Beside<T> P(static_cast<const T*>(a.target) + ((size_t)b * a.Kt + k) * a.V, a.V, D);
     const float g = a.g_kl[r];
     if (P.aligned())
-        kl_grad_tile<T, true>(a, D, P, out, whole, tile, s, g);
+        kl_grad_tile<T, ONCE, true>(a, D, P, out, whole, tile, s, g);
     else
-        kl_grad_tile<T, false>(a, D, P, out, whole, tile, s, g);
+        kl_grad_tile<T, ONCE, false>(a, D, P, out, whole, tile, s, g);
 }
 
 // ---------------------------------------------------------------- host side
@@ -808,14 +810,28 @@ inline Split split_of(spec_dtype d, long long rows, int V) {
     const int chunk = (steps + parts - 1) / parts * kThreads;
     return {(nvec + chunk - 1) / chunk, chunk};
 }
-// A workgroup that reads one 4 KiB step takes one block a thread.
-template <typename T>
-void launch_logprobs(const LpArgs& a, unsigned grid, hipStream_t st) {
-    const bool one = a.chunk == kThreads;
-    if (a.top_n)
-        one ? k_logprobs<T, true, 1><<<grid, kThreads, 0, st>>>(a) : k_logprobs<T, true, kUnroll><<<grid, kThreads, 0, st>>>(a);
+// Logits beyond what the chip's caches hold are read past them: nothing would
+// be left of them for the gradient (log probs with their gradient, 2048 rows of
+// 151936 bf16: 323 us, 349 with temporal loads; 160 rows of 128256 of KL are
+// slower so, 48.5 and 46.3).
+inline bool read_once(spec_dtype d, long long rows, int V) {
+    return rows * V * (d == SPEC_BF16 ? 2 : 4) > (256ll << 20);
+}
+
+// A workgroup that reads one 4 KiB step takes one block a thread.  Rows that
+// are read once are many, so none is split into single steps.
+template <typename T, bool TOP>
+void launch_logprobs(const LpArgs& a, bool once, unsigned grid, hipStream_t st) {
+    if (once)
+        k_logprobs<T, TOP, kUnroll, true><<<grid, kThreads, 0, st>>>(a);
+    else if (a.chunk == kThreads)
+        k_logprobs<T, TOP, 1, false><<<grid, kThreads, 0, st>>>(a);
     else
-        one ? k_logprobs<T, false, 1><<<grid, kThreads, 0, st>>>(a) : k_logprobs<T, false, kUnroll><<<grid, kThreads, 0, st>>>(a);
+        k_logprobs<T, TOP, kUnroll, false><<<grid, kThreads, 0, st>>>(a);
+}
+template <typename T>
+void launch_logprobs(const LpArgs& a, bool once, unsigned grid, hipStream_t st) {
+    a.top_n ? launch_logprobs<T, true>(a, once, grid, st) : launch_logprobs<T, false>(a, once, grid, st);
 }
 
 // Counters of the rows, then `words` 8-byte words for each part of each row.
@@ -849,9 +865,9 @@ extern "C" spec_status spec_token_logprobs(const void* logits, spec_dtype dtype,
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const unsigned grid = (unsigned)rows * (unsigned)s.parts;
     if (dtype == SPEC_BF16)
-        launch_logprobs<uint16_t>(a, grid, st);
+        launch_logprobs<uint16_t>(a, read_once(dtype, rows, V), grid, st);
     else
-        launch_logprobs<float>(a, grid, st);
+        launch_logprobs<float>(a, read_once(dtype, rows, V), grid, st);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
@@ -866,10 +882,11 @@ extern "C" spec_status spec_token_logprobs_grad(const void* logits, spec_dtype d
     const LpGradArgs a{logits, tokens, stats, grad_logprob, grad_entropy, rows, V, tiles, out_grad};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const unsigned grid = (unsigned)rows * (unsigned)tiles;
+    const bool once = read_once(dtype, rows, V);
     if (dtype == SPEC_BF16)
-        k_logprobs_grad<uint16_t><<<grid, kThreads, 0, st>>>(a);
+        once ? k_logprobs_grad<uint16_t, true><<<grid, kThreads, 0, st>>>(a) : k_logprobs_grad<uint16_t, false><<<grid, kThreads, 0, st>>>(a);
     else
-        k_logprobs_grad<float><<<grid, kThreads, 0, st>>>(a);
+        once ? k_logprobs_grad<float, true><<<grid, kThreads, 0, st>>>(a) : k_logprobs_grad<float, false><<<grid, kThreads, 0, st>>>(a);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
@@ -897,10 +914,11 @@ extern "C" spec_status spec_draft_kl(const void* target_logits, const void* draf
                    reinterpret_cast<uint64_t*>(ws + counter_bytes((long long)B * K))};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const unsigned grid = (unsigned)(B * K) * (unsigned)s.parts;
+    const bool once = read_once(dtype, (long long)B * K, V);
     if (dtype == SPEC_BF16)
-        k_draft_kl<uint16_t><<<grid, kThreads, 0, st>>>(a);
+        once ? k_draft_kl<uint16_t, true><<<grid, kThreads, 0, st>>>(a) : k_draft_kl<uint16_t, false><<<grid, kThreads, 0, st>>>(a);
     else
-        k_draft_kl<float><<<grid, kThreads, 0, st>>>(a);
+        once ? k_draft_kl<float, true><<<grid, kThreads, 0, st>>>(a) : k_draft_kl<float, false><<<grid, kThreads, 0, st>>>(a);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
 
@@ -915,9 +933,10 @@ extern "C" spec_status spec_draft_kl_grad(const void* target_logits, const void*
     const KlArgs a{target_logits, draft_logits, mask, K, target_rows, V, tiles, nullptr, const_cast<float*>(stats), grad_kl, out_grad, 1, 0, nullptr, nullptr};
     const hipStream_t st = static_cast<hipStream_t>(stream);
     const unsigned grid = (unsigned)(B * K) * (unsigned)tiles;
+    const bool once = read_once(dtype, (long long)B * K, V);
     if (dtype == SPEC_BF16)
-        k_draft_kl_grad<uint16_t><<<grid, kThreads, 0, st>>>(a);
+        once ? k_draft_kl_grad<uint16_t, true><<<grid, kThreads, 0, st>>>(a) : k_draft_kl_grad<uint16_t, false><<<grid, kThreads, 0, st>>>(a);
     else
-        k_draft_kl_grad<float><<<grid, kThreads, 0, st>>>(a);
+        once ? k_draft_kl_grad<float, true><<<grid, kThreads, 0, st>>>(a) : k_draft_kl_grad<float, false><<<grid, kThreads, 0, st>>>(a);
     return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_EHIP;
 }
