@@ -128,8 +128,9 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {  // round to nearest 
 __device__ inline float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }  // 0 below 2^-126
 
 // A row's gradient, written block by block like Row reads: whole blocks at
-// once where the output row is aligned like the input row.
-template <typename T>
+// once where the output row is aligned like the input row; ONCE: past the
+// caches too.
+template <bool ONCE, typename T>
 __device__ inline void store_block(T* row, const Row<T>& r, int i, bool whole, const float (&v)[Row<T>::kVec]) {
     constexpr int kVec = Row<T>::kVec;
     const int e = r.first(i);
@@ -142,7 +143,10 @@ __device__ inline void store_block(T* row, const Row<T>& r, int i, bool whole, c
         for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(v[j]);
     }
     if (whole && e >= 0 && e + kVec <= r.stop) {
-        *reinterpret_cast<u32x4*>(row + e) = q;
+        if constexpr (ONCE)
+            __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(row + e));
+        else
+            *reinterpret_cast<u32x4*>(row + e) = q;
         return;
     }
 #pragma unroll
@@ -397,9 +401,10 @@ __device__ inline bool last_to_come(uint32_t* counter, int parts) {
 // logits above the last one kept (their indices are higher, so a tie loses).
 // U: blocks per thread and tile.  The next tile is loaded while one is worked
 // on.
-// Bound by reading where there are many rows: 2048 rows of 151936 bf16 take
-// 110 us (5.7 TB/s), 160 us with 20 alternatives, whose scan for candidates
-// costs about as many instructions as the statistics.  144 rows of 128256 take
+// Bound by reading where there are many rows: 1844 rows of 151936 bf16 take 94
+// us (6.0 TB/s); 2048 rows through the caches 110 us, and 160 us with 20
+// alternatives, whose scan for candidates costs about as many instructions as
+// the statistics.  144 rows of 128256 take
 // 14 us (2.6 TB/s), 25 us with 20; six rows 7.5 and 12.5 us: there it is the
 // launch, the join and the fold, one after the other.
 template <typename T, bool TOP, int U, bool ONCE>
@@ -580,8 +585,7 @@ struct LpGradArgs {
 };
 
 // One workgroup per tile of a row: reads its logits and writes their gradient,
-// bound by both: 192 us for 2048 rows of 151936 bf16, a tenth of them padded
-// and only written (6.2 TB/s).
+// bound by both.
 template <typename T, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
     constexpr int kVec = Row<T>::kVec;
@@ -614,7 +618,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j) v[j] = 0.f;
         }
-        store_block(out, R, i, whole, v);
+        store_block<ONCE>(out, R, i, whole, v);
     }
 }
 
@@ -634,7 +638,8 @@ struct KlArgs {
 
 // Split over workgroups like k_logprobs.  Blocks follow the target's row.
 // Bound by reading both rows and, close behind, by two exponentials a token:
-// 205 us for 1844 rows of 128255 bf16 (4.6 TB/s), 23 us for 128 of 128256.
+// 177 us for 1844 rows of 128255 bf16 (5.3 TB/s), 205 through the caches; 23 us
+// for 128 of 128256.
 template <typename T, bool ONCE, bool ALIGNED>
 __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, Pair& st) {
     constexpr int kVec = Row<T>::kVec;
@@ -721,8 +726,9 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
     }
 }
 
-// One workgroup per tile of a draft row: reads both rows, writes the gradient:
-// 247 us for 2048 rows of 128255 bf16, a tenth of them masked (6.0 TB/s).
+// One workgroup per tile of a draft row: reads both rows, writes the gradient,
+// bound by that: forward and gradient of 2048 rows of 128255 bf16, a tenth of
+// them masked, take 454 us for 2.4 GB (5.3 TB/s).
 template <typename T, bool ONCE, bool ALIGNED>
 __device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Beside<T>& P, T* out, bool whole, int tile, const float4& s, float g) {
     constexpr int kVec = Row<T>::kVec;
@@ -743,7 +749,7 @@ __device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Besi
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
             q[j] = g * (exp2_(((q[j] - s.z) - s.w) * kLog2e) - exp2_(((p[j] - s.x) - s.y) * kLog2e));
-        store_block(out, D, i, whole, q);
+        store_block<ONCE>(out, D, i, whole, q);
     }
 }
 
@@ -762,7 +768,7 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl_grad(KlArgs a) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int i = tile * kTileVecs + u * kThreads + t;
-            if (i < D.nvec) store_block(out, D, i, whole, zero);
+            if (i < D.nvec) store_block<ONCE>(out, D, i, whole, zero);
         }
         return;
     }
@@ -810,10 +816,11 @@ inline Split split_of(spec_dtype d, long long rows, int V) {
     const int chunk = (steps + parts - 1) / parts * kThreads;
     return {(nvec + chunk - 1) / chunk, chunk};
 }
-// Logits beyond what the chip's caches hold are read past them: nothing would
-// be left of them for the gradient (log probs with their gradient, 2048 rows of
-// 151936 bf16: 323 us, 349 with temporal loads; 160 rows of 128256 of KL are
-// slower so, 48.5 and 46.3).
+// Logits beyond what the chip's caches hold are read past them, and their
+// gradients written past them: nothing would be left there for the next reader
+// (log probs with their gradient, 2048 rows of 151936 bf16: 349 us through the
+// caches, 323 with the loads past them, 299 with the stores too; 160 rows of
+// 128256 of KL are slower so, 48.5 and 46.3).
 inline bool read_once(spec_dtype d, long long rows, int V) {
     return rows * V * (d == SPEC_BF16 ? 2 : 4) > (256ll << 20);
 }

@@ -523,3 +523,38 @@ def test_rows_past_32_bits_of_offset():
     one = sv.spec_token_logprobs(X[-1:].clone(), tok[-1:], top_n=3)
     assert torch.equal(r.logprob[-1:], one.logprob) or (r.logprob[-1] - one.logprob[0]).abs() < 1e-5
     assert torch.equal(r.top_tokens[-1:], one.top_tokens) and (r.logprob[:-1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1100), ("f32", 1030)])
+@pytest.mark.parametrize("V", [128256, 128255])
+def test_rows_beyond_the_caches(V, rows, dtype):
+    """Logits of more than 256 MiB, which are read and whose gradients are
+    written past the caches, equal their halves' results bit for bit."""
+    X = rows_of(rows, V, DT[dtype], 21).requires_grad_()
+    tok = tokens_of(rows, V, 21)
+    tok[::7] = -1
+    assert X.numel() * X.element_size() > 256 << 20
+    w = torch.rand(rows, device="cuda")
+
+    def run(x, t, w, draft):
+        r = sv.spec_token_logprobs(x, t, top_n=3)
+        g, = torch.autograd.grad([r.logprob, r.entropy], [x], [w, 1 - w])
+        kl = sv.spec_draft_kl(draft, x[None], mask=(t >= 0)[None])
+        gk, = torch.autograd.grad([kl], [x], [w[None]])
+        return [v.detach() for v in (*r, g, kl[0], gk)]
+
+    T = rows_of(rows, V, DT[dtype], 22)
+    def piece(x, s):
+        """A copy of some rows that starts at the same place of 16 bytes: the
+        order of a row's sums follows its alignment."""
+        x = x.detach()
+        off = s.start * V % (16 // x.element_size())
+        buf = torch.empty(x[s].numel() + off, dtype=x.dtype, device="cuda")
+        buf[off:] = x[s].reshape(-1)
+        return buf[off:].view(-1, V)
+
+    whole = run(X, tok, w, T[None])
+    for half in (slice(0, rows // 2), slice(rows // 2, rows)):
+        part = run(piece(X, half).requires_grad_(), tok[half], w[half], piece(T, half)[None])
+        for a, b in zip(whole, part):
+            assert torch.equal(a[half], b)
