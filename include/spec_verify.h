@@ -489,7 +489,7 @@ spec_status spec_verify_exact_noalloc(const void *target_logits, const void *dra
  * Operators on logit rows beside the rules.  Rows, dtype, alignment, streams
  * and errors as above; a row may hold -inf entries (probability zero) and
  * values down to the type's lowest, and may hold nothing but -inf.  A row with
- * a NaN or +inf gives NaN results (alternatives: any tokens of [0, V)).
+ * a NaN or +inf gives NaN results (alternatives: any tokens of [0, V), or -1).
  * Limits: rows * (tiles of 16 KiB a row, one more where rows are not 16-byte
  * aligned) < 2^24.  Sums, maxima and the log-probs are fp32.  Workspaces are
  * 256-byte aligned and zero-filled before their first use; every call leaves
