@@ -610,7 +610,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float lp = (v[j] - ref) - ls, p = exp2_(lp * kLog2e);
-                float g = -p * fmaf(ge, fmaxf(lp, -3.0e38f) + H, gl);
+                // p first: it bounds what lp + H and any weight can grow to
+                float g = p == 0.f ? 0.f : -fmaf(ge, p * (lp + H), gl * p);
                 if (R.first(i) + j == x) g += gl;
                 v[j] = g;
             }

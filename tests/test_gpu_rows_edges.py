@@ -1,0 +1,64 @@
+"""Edges of spec_token_logprobs and spec_draft_kl: gradients of any weight on
+masked rows, terms at the ends of the exponent range.  Against float64, with
+the bounds of test_gpu_rows.py.
+"""
+import math
+
+import pytest
+import torch
+
+import draft_verification_row_amd as sv
+from test_gpu_rows import DT, Ref, close, half, rows_of, tokens_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("weight", [1.2, 1.5, 100.0, 65536.0, 1e30])
+@pytest.mark.parametrize("V", [33, 16500])
+def test_entropy_gradient_of_any_weight(V, weight, dtype):
+    """Entropy gradients of either sign on rows with -inf and the type's lowest
+    value in places: 0 where p = 0, the formula elsewhere."""
+    dt = DT[dtype]
+    X = rows_of(8, V, dt, seed=9).clone()
+    tok = tokens_of(8, V, 9)
+    X[0:2, ::3] = -math.inf
+    X[2:4, ::2] = torch.finfo(dt).min
+    X[4:6, : V - 2] = -math.inf
+    X[6:8] = torch.finfo(dt).min
+    X[6:8, 5] = 3.0
+    X.requires_grad_()
+    ref = Ref(X, tok)
+    ge = weight * torch.tensor([1.0, -1.0], device="cuda").repeat(4)
+    gl = torch.linspace(-1, 1, 8, device="cuda")
+    r = sv.spec_token_logprobs(X, tok)
+    for a in (gl, None):
+        outs, ws = ([r.logprob, r.entropy], [gl, ge]) if a is not None else ([r.entropy], [ge])
+        got, = torch.autograd.grad(outs, [X], ws, retain_graph=True)
+        want, err = ref.grad(torch.zeros_like(gl) if a is None else a, ge)
+        close(got, want, err + half(dt) * want.abs() + 1e-38, "grad")
+        # a masked place's gradient is exactly 0, but for the row's own token
+        masked = (ref.p == 0).scatter(1, ref.at, False)
+        assert (got[masked] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_entropy_gradient_of_a_scaled_loss(dtype):
+    """(2 * entropy).sum().backward() under a sampling mask."""
+    X = rows_of(4, 5000, DT[dtype], seed=2).clone()
+    X[:, 100:] = -math.inf
+    X.requires_grad_()
+    (2 * sv.spec_token_logprobs(X, tokens_of(4, 100, 3)).entropy).sum().backward()
+    assert X.grad.isfinite().all() and (X.grad[:, 100:] == 0).all() and (X.grad[:, :100] != 0).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_rows_have_nan_gradients(dtype):
+    """A NaN logit stays visible in its own row's gradient, and in no other."""
+    X = rows_of(3, 4000, DT[dtype], seed=4).clone()
+    X[1, 7] = math.nan
+    X[:, 9] = -math.inf
+    X.requires_grad_()
+    r = sv.spec_token_logprobs(X, tokens_of(3, 4000, 5))
+    g, = torch.autograd.grad((r.logprob + 3 * r.entropy).sum(), [X])
+    assert g[1].isnan().all() and g[0].isfinite().all() and g[2].isfinite().all()
