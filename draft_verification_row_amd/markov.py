@@ -119,13 +119,18 @@ def _round(m, cur, udt_r, uv_r, ws, rows, emitted_r, accept_r):
     (udt_r [K][B]: draft step i's uniforms are row i), one exact verification;
     writes the round's outputs and returns the next cur.  rows = arange(B)."""
     K = udt_r.shape[0]
+    if K < 1:
+        raise SpecVerifyError("K must be positive")
     ws_s, ws_v = ws
-    prev = [cur]
+    prev, steps = [cur], []
     for i in range(K):
-        d = spec_sample_drafts(_logits(m.draft, prev[-1], m.dtype), udt_r[i], logprobs=False, workspace=ws_s)
-        prev.append(d.tokens)
+        q = _logits(m.draft, prev[-1], m.dtype)
+        prev.append(spec_sample_drafts(q, udt_r[i], logprobs=False, workspace=ws_s).tokens)
+        steps.append(q)
     idx = torch.stack(prev, 1)
-    res = spec_verify_exact(_logits(m.target, idx, m.dtype), _logits(m.draft, idx[:, :K], m.dtype),
+    # the rule takes the very logits the drafts were drawn from: a head's would
+    # come out a rounding apart if all K steps were computed at once
+    res = spec_verify_exact(_logits(m.target, idx, m.dtype), torch.stack(steps, 1),
                             idx[:, 1:].contiguous(), uv_r, logprobs=False, workspace=ws_v)
     emitted_r.copy_(res.tokens)
     accept_r.copy_(res.accept_len)

@@ -1,0 +1,44 @@
+"""The driver on draft heads: what it hands to the rule, and what it keeps."""
+import pytest
+import torch
+
+import draft_verification_row_amd as sv
+import draft_verification_row_amd.markov as mk
+from test_gpu_heads import head
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("B,K,H,blocks", [(12, 3, 64, 1), (4, 5, 512, 2), (16, 8, 96, 0), (1, 1, 64, 1), (33, 2, 64, 1)])
+def test_the_rule_gets_the_logits_the_drafts_were_drawn_from(monkeypatch, B, K, H, blocks):
+    """Bit for bit, also where B rows and B * K rows take different kernels of
+    the product (B = 12, K = 3: 12 rows and 36)."""
+    V, rounds = 300, 3
+    draft = head(V, H, blocks, torch.bfloat16, 1)
+    target = (torch.randn(V, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)) * 2).bfloat16()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    start = torch.randint(0, V, (B,), dtype=torch.int32, device="cuda", generator=g)
+    ud = torch.rand(rounds, B, K, device="cuda", generator=g)
+    uv = torch.rand(rounds, B, K + 1, device="cuda", generator=g)
+    drawn, given = [], []
+    sample, verify = mk.spec_sample_drafts, mk.spec_verify_exact
+
+    def sampled(q, *a, **k):
+        drawn.append(q.clone())
+        return sample(q, *a, **k)
+
+    def verified(T, D, x, *a, **k):
+        given.append((D.clone(), x.clone()))
+        return verify(T, D, x, *a, **k)
+
+    monkeypatch.setattr(mk, "spec_sample_drafts", sampled)
+    monkeypatch.setattr(mk, "spec_verify_exact", verified)
+    tr = mk.generate_speculative(target, draft, start, ud, uv)
+    monkeypatch.undo()
+    assert len(drawn) == rounds * K and len(given) == rounds
+    for r in range(rounds):
+        assert torch.equal(given[r][0], torch.stack(drawn[r * K:(r + 1) * K], 1)), r
+    # and the captured driver makes the same calls
+    out = mk.SpeculativeGraph(target, draft, B, K, rounds).run(start, ud, uv)
+    torch.cuda.synchronize()
+    assert torch.equal(out.emitted, tr.emitted) and torch.equal(out.accept_len, tr.accept_len)
