@@ -47,7 +47,7 @@ def head_logits(model: HeadModel, tokens: torch.Tensor, *,
     """The model's next-token logits after each of `tokens` (an integer tensor
     on the GPU): [*tokens.shape][V] in out_dtype (the model's by default).  The
     parameters have gradients."""
-    h = model.embedding[tokens]
+    h = model.embedding[tokens].contiguous()  # a view of tokens gives a view
     for weight, bias in model.blocks:
         h = spec_linear(h, weight, bias, residual=h, activation="silu")
     return spec_linear(h, model.output, out_dtype=out_dtype)

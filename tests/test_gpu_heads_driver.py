@@ -42,3 +42,19 @@ def test_the_rule_gets_the_logits_the_drafts_were_drawn_from(monkeypatch, B, K, 
     out = mk.SpeculativeGraph(target, draft, B, K, rounds).run(start, ud, uv)
     torch.cuda.synchronize()
     assert torch.equal(out.emitted, tr.emitted) and torch.equal(out.accept_len, tr.accept_len)
+
+
+def test_head_logits_of_views_of_tokens():
+    """Any integer tensor of tokens, whatever its strides."""
+    m = head(200, 64, 2, torch.bfloat16, 4)
+    tok = torch.randint(0, 200, (6, 10, 4), device="cuda")
+    for view in (tok.transpose(0, 1), tok[:, ::2, 1:3], tok[0, 0].expand(5, 4), tok.int().permute(2, 0, 1), tok[1, 2, 3]):
+        got = mk.head_logits(m, view)
+        assert got.shape == (*view.shape, 200) and torch.equal(got, mk.head_logits(m, view.contiguous()))
+    # and with a gradient to the embedding: the rows' sums, of at most 240 terms
+    # in float32, may be added in another order
+    m = head(200, 64, 1, torch.float32, 4)
+    m = m._replace(embedding=m.embedding.requires_grad_())
+    a, b = (torch.autograd.grad(mk.head_logits(m, t).sum(), [m.embedding])[0]
+            for t in (tok.transpose(0, 1), tok.transpose(0, 1).contiguous()))
+    assert (a - b).abs().max() < 1e-4 * b.abs().max()
