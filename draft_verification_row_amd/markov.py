@@ -95,7 +95,14 @@ def _models(target, draft) -> _Models:
         raise SpecVerifyError(f"draft_table must have target_table's vocabulary {V} and dtype "
                               f"{dtype}, got {Vd} and {dd}")
     dev = (target.embedding if isinstance(target, HeadModel) else target).device
-    return _Models(target, draft, V, dtype, dev)
+    return _Models(_held(target), _held(draft), V, dtype, dev)
+
+
+def _held(model):
+    """The model with its blocks in tuples, which no one else can change."""
+    if isinstance(model, HeadModel):
+        return model._replace(blocks=tuple((weight, bias) for weight, bias in model.blocks))
+    return model
 
 
 def _logits(model, tokens, dtype):
@@ -181,7 +188,9 @@ class SpeculativeGraph:
         self.accept = torch.empty((rounds, B), dtype=torch.int32, device=dev)
         # Buffers made before the capture and read by the graph belong to the
         # ordinary allocator, so they are held here for the graph's lifetime:
-        # freed, their blocks could go to other tensors between replays.
+        # freed, their blocks could go to other tensors between replays.  The
+        # heads' tensors too, whatever becomes of the caller's list of blocks.
+        self._models = m
         self._ws = _workspaces(m, B, K)
         self._rows = torch.arange(B, dtype=torch.int32, device=dev)
         self.graph = torch.cuda.CUDAGraph()

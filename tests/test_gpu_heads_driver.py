@@ -58,3 +58,26 @@ def test_head_logits_of_views_of_tokens():
     a, b = (torch.autograd.grad(mk.head_logits(m, t).sum(), [m.embedding])[0]
             for t in (tok.transpose(0, 1), tok.transpose(0, 1).contiguous()))
     assert (a - b).abs().max() < 1e-4 * b.abs().max()
+
+
+def test_a_captured_driver_keeps_its_heads_tensors():
+    """A head's list of blocks that is changed after the capture: the graph
+    still reads the weights it was captured with."""
+    V, H, B, K, rounds = 300, 512, 4, 3, 2
+    model = head(V, H, 2, torch.bfloat16, 1)
+    blocks = list(model.blocks)
+    draft = model._replace(blocks=blocks)
+    target = (torch.randn(V, V, device="cuda") * 2).bfloat16()
+    start = torch.randint(0, V, (B,), dtype=torch.int32, device="cuda")
+    ud, uv = torch.rand(rounds, B, K, device="cuda"), torch.rand(rounds, B, K + 1, device="cuda")
+    g = mk.SpeculativeGraph(target, draft, B, K, rounds)
+    want = [t.clone() for t in g.run(start, ud, uv)]
+    torch.cuda.synchronize()
+    del model
+    held = [weight.data_ptr() for weight, _ in blocks]
+    blocks.clear()
+    fill = [torch.full((H, H), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(8)]
+    assert not {t.data_ptr() for t in fill} & set(held)
+    out = g.run(start, ud, uv)
+    torch.cuda.synchronize()
+    assert torch.equal(out.emitted, want[0]) and torch.equal(out.accept_len, want[1])
