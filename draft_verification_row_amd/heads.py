@@ -47,11 +47,18 @@ def _stream(index: int) -> int:
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
 
 
+def _workspace_bytes(query: str, *sizes: int) -> int:
+    """The library's answer to a size query; what it does not take, and what
+    its 32-bit sizes cannot hold, is refused."""
+    n = getattr(load_library(), query)(*sizes) if max(sizes) < 1 << 31 else 0
+    if n == 0:
+        raise SpecVerifyError("sizes outside the supported range")
+    return n
+
+
 def _zeroed(device: torch.device, nbytes: int) -> torch.Tensor:
     """A zero-filled workspace: one per (device, stream) for eager calls, a
     fresh one for a captured call, so that graphs share none."""
-    if nbytes == 0:
-        raise SpecVerifyError("sizes outside the supported range")
     if torch.cuda.is_current_stream_capturing():
         return torch.zeros(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, _stream(device.index))
@@ -125,7 +132,7 @@ def _logprobs(X, tokens, top_n, stats):
     st = torch.empty((*lead, 4), **f32) if stats else None
     if rows:
         code = _dtype_code(X)
-        ws = _zeroed(dev, load_library().spec_logprobs_workspace_bytes(code, rows, V, top_n))
+        ws = _zeroed(dev, _workspace_bytes("spec_logprobs_workspace_bytes", code, rows, V, top_n))
         _call("spec_token_logprobs", dev, _p(X), code, _p(tokens), rows, V, top_n, _p(out.logprob),
               _p(out.entropy), _p(out.top_tokens), _p(out.top_logprob), _p(out.status), _p(st),
               _p(ws), ws.numel())
@@ -189,7 +196,7 @@ def _kl(T, D, mask, stats):
     st = torch.empty((B, K, 4), dtype=torch.float32, device=D.device) if stats else None
     if B * K:
         code = _dtype_code(D)
-        ws = _zeroed(D.device, load_library().spec_draft_kl_workspace_bytes(code, B, K, V))
+        ws = _zeroed(D.device, _workspace_bytes("spec_draft_kl_workspace_bytes", code, B, K, V))
         _call("spec_draft_kl", D.device, _p(T), _p(D), code, _p(mask), B, K, T.shape[1], V,
               _p(kl), _p(st), _p(ws), ws.numel())
     return kl, st
@@ -226,7 +233,7 @@ def spec_draft_kl(target_logits: torch.Tensor, draft_logits: torch.Tensor, *,
     if T.dim() != 3 or D.dim() != 3 or D.shape[2] < 1:
         raise SpecVerifyError("target_logits must be [B][K+1][V] and draft_logits [B][K][V]")
     B, K, V = D.shape
-    if T.shape[0] != B or T.shape[2] != V or T.shape[1] < K:
+    if T.shape[0] != B or T.shape[2] != V or not K <= T.shape[1] < 1 << 31:
         raise SpecVerifyError(f"target_logits has shape {tuple(T.shape)}, expected "
                               f"{(B, K + 1, V)} or {(B, K, V)}")
     _dtype_code(D)
@@ -252,18 +259,11 @@ def _linear(x, weight, bias, residual, act, out_dtype, preact):
     z = torch.empty((M, N), dtype=x.dtype, device=x.device) if preact else None
     if M:
         code = _dtype_code(x)
-        ws = torch.empty(_linear_bytes("spec_linear_workspace_bytes", code, M, N, K),
+        ws = torch.empty(_workspace_bytes("spec_linear_workspace_bytes", code, M, N, K),
                          dtype=torch.uint8, device=x.device)
         _call("spec_linear", x.device, _p(x), _p(weight), _p(bias), _p(residual), code,
               _dtype_code(out), act, M, N, K, _p(out), _p(z), _p(ws), ws.numel())
     return out, z
-
-
-def _linear_bytes(query, *sizes) -> int:
-    n = getattr(load_library(), query)(*sizes)
-    if n == 0:
-        raise SpecVerifyError("sizes outside the supported range")
-    return n
 
 
 class _Linear(torch.autograd.Function):
@@ -293,7 +293,7 @@ class _Linear(torch.autograd.Function):
         if M and any(need[:3]):
             g = g_y.contiguous()
             code = 1 if dtype == torch.bfloat16 else 0
-            ws = torch.empty(_linear_bytes("spec_linear_grad_workspace_bytes", code, M, N, K),
+            ws = torch.empty(_workspace_bytes("spec_linear_grad_workspace_bytes", code, M, N, K),
                              dtype=torch.uint8, device=dev)
             _call("spec_linear_grad", dev, _p(x), _p(weight), _p(z), _p(g), code, _dtype_code(g),
                   ctx.act, M, N, K, _p(gx), _p(gw), _p(gb), _p(ws), ws.numel())
