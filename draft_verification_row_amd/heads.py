@@ -47,6 +47,15 @@ def _stream(index: int) -> int:
 _stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
 
 
+def _capturing(index: int) -> bool:
+    """Whether the device's current stream, which the calls run on, is being
+    captured: torch answers for the current device alone."""
+    if index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _workspace_bytes(query: str, *sizes: int) -> int:
     """The library's answer to a size query; what it does not take, and what
     its 32-bit sizes cannot hold, is refused."""
@@ -59,7 +68,7 @@ def _workspace_bytes(query: str, *sizes: int) -> int:
 def _zeroed(device: torch.device, nbytes: int) -> torch.Tensor:
     """A zero-filled workspace: one per (device, stream) for eager calls, a
     fresh one for a captured call, so that graphs share none."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(device.index):
         return torch.zeros(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, _stream(device.index))
     ws = _workspaces.get(key)
@@ -103,7 +112,7 @@ def _mark_leaves(out: torch.Tensor) -> None:
     living graph of these operators made on another stream is refused in a
     capture."""
     _note_stream(out.grad_fn.next_functions, _stream(out.device.index),
-                 torch.cuda.is_current_stream_capturing())
+                 _capturing(out.device.index))
 
 
 def _note_stream(edges, stream: int, capturing: bool) -> None:

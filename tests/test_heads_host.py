@@ -17,3 +17,32 @@ def test_sizes_past_32_bits_are_refused(wrap):
             with pytest.raises(sv.SpecVerifyError):
                 heads._workspace_bytes(query, *(n + wrap * (j == i) for j, n in enumerate(sizes)))
                 print("not refused:", query, i)
+
+
+def test_a_capture_on_another_device_is_seen(monkeypatch):
+    """Tensors of device 1 while device 0 is current: device 1's stream
+    decides whether a call is captured and gets a workspace of its own."""
+    import torch
+    state = {"device": 0, "capturing": {1}}
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, state["device"] = state["device"], self.index
+
+        def __exit__(self, *_):
+            state["device"] = self.before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: state["device"])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["device"] in state["capturing"])
+    monkeypatch.setattr(heads, "_stream", lambda index: 7)
+    made = []
+    monkeypatch.setattr(torch, "zeros", lambda n, **k: made.append(k["device"]) or torch.empty(n, dtype=torch.uint8))
+    monkeypatch.setattr(heads, "_workspaces", {})
+    one, two = (heads._zeroed(torch.device("cuda", 1), 256) for _ in range(2))
+    assert one is not two and len(made) == 2 and not heads._workspaces and state["device"] == 0
+    three, four = (heads._zeroed(torch.device("cuda", 0), 256) for _ in range(2))  # not captured: kept
+    assert three is four and list(heads._workspaces) == [(0, 7)]
