@@ -9,7 +9,7 @@ carry one (first order).  Calls may be captured into a graph: a captured call
 gets a workspace of its own, which lives as long as the graph.  Before a
 backward pass is captured, graphs of the same leaves that were built on other
 streams have to be gone (the capture is refused while one of these operators'
-lives).
+lives, of leaves that they take as they are or cast, viewed or looked up).
 """
 from __future__ import annotations
 
@@ -110,9 +110,25 @@ def _mark_leaves(out: torch.Tensor) -> None:
     pass that is captured on another stream would draw that stream into the
     capture, which ends the process.  So a leaf whose node an earlier, still
     living graph of these operators made on another stream is refused in a
-    capture."""
-    _note_stream(out.grad_fn.next_functions, _stream(out.device.index),
-                 _capturing(out.device.index))
+    capture.  A leaf counts where an operator takes it, and behind casts, views,
+    lookups and whatever else has one input that requires a gradient."""
+    _note_stream([(_behind(node), 0) for node, _ in out.grad_fn.next_functions],
+                 _stream(out.device.index), _capturing(out.device.index))
+
+
+_CHAIN = 8  # nodes that are looked past; each costs about a microsecond
+
+
+def _behind(node):
+    """The gradient node behind up to _CHAIN nodes of one edge each."""
+    for _ in range(_CHAIN):
+        if node is None or type(node).__name__ == "AccumulateGrad":
+            break
+        edges = [n for n, _ in node.next_functions if n is not None]
+        if len(edges) != 1:
+            break
+        node = edges[0]
+    return node
 
 
 def _note_stream(edges, stream: int, capturing: bool) -> None:

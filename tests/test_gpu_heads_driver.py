@@ -81,3 +81,44 @@ def test_a_captured_driver_keeps_its_heads_tensors():
     out = g.run(start, ud, uv)
     torch.cuda.synchronize()
     assert torch.equal(out.emitted, want[0]) and torch.equal(out.accept_len, want[1])
+
+
+def test_a_captured_step_of_cast_weights_is_refused_while_an_eager_one_lives():
+    """float32 weights, cast for each call: the eager graph has to go first;
+    then the step is captured and its replays equal the eager gradients."""
+    V, H = 150, 64
+    m = head(V, H, 1, torch.float32, 6)
+    (w, b), out = m.blocks[0], m.output
+    ps = [w.requires_grad_(), b.requires_grad_(), out.requires_grad_()]
+    emb = m.embedding.bfloat16()
+    tok = torch.randint(0, V, (5, 3), device="cuda")
+    gy = torch.randn(5, 3, V, device="cuda")
+
+    def forward():
+        return mk.head_logits(mk.HeadModel(emb, [(w.bfloat16(), b.bfloat16())], out.bfloat16()), tok, out_dtype=torch.float32)
+
+    def step():
+        return torch.autograd.grad([forward()], ps, [gy])
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want = [g.clone() for g in step()]
+    torch.cuda.current_stream().wait_stream(s)
+    kept = forward()
+    with pytest.raises(sv.SpecVerifyError):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            forward()
+    torch.cuda.synchronize()
+    del kept
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for rep in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), rep
+        step()
+        torch.cuda.synchronize()

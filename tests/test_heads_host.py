@@ -46,3 +46,34 @@ def test_a_capture_on_another_device_is_seen(monkeypatch):
     assert one is not two and len(made) == 2 and not heads._workspaces and state["device"] == 0
     three, four = (heads._zeroed(torch.device("cuda", 0), 256) for _ in range(2))  # not captured: kept
     assert three is four and list(heads._workspaces) == [(0, 7)]
+
+
+@pytest.mark.parametrize("taken", ["as is", "cast", "viewed", "looked up", "cast, looked up and viewed"])
+def test_a_capture_refuses_leaves_behind_one_input_operators(monkeypatch, taken):
+    """A weight kept in float32 and cast for each call, a view of it, an
+    embedding's rows: the leaf behind is the one whose node counts."""
+    import torch
+    now = {"stream": 1, "capturing": False}
+    monkeypatch.setattr(heads, "_stream", lambda index: now["stream"])
+    monkeypatch.setattr(heads, "_capturing", lambda index: now["capturing"])
+    leaf = torch.ones(6, 4, requires_grad=True)
+    take = {"as is": lambda t: t, "cast": lambda t: t.to(torch.float64), "viewed": lambda t: t.t().reshape(4, 6).t(),
+            "looked up": lambda t: t[torch.tensor([1, 5])],
+            "cast, looked up and viewed": lambda t: t.double()[torch.tensor([1, 5])].contiguous().view(2, 4)}[taken]
+
+    def call():  # an operator of two inputs, one of them new
+        out = take(leaf) * torch.ones(4, requires_grad=True)
+        heads._mark_leaves(out)
+        return out
+
+    kept = call()
+    now.update(stream=2)
+    call()                                  # eager: any stream
+    now.update(capturing=True)
+    with pytest.raises(sv.SpecVerifyError):
+        call()
+    now.update(stream=1)
+    call()                                  # captured on the same stream
+    del kept
+    now.update(stream=2)
+    call()                                  # the graphs are gone
