@@ -181,26 +181,27 @@ __device__ inline Soft join(const Soft& x, const Soft& y) {
     return {m, p.s + q.s, p.a + q.a};
 }
 
-struct Pair {  // of two rows' logits: maxima, sums, and U of the comment above
-    float m, s, n, r, u;
+struct Pair {  // of two rows' logits: maxima, sums, U of the comment above, and
+    float m, s, n, r, u, w;  // the largest target logit under a draft's -inf
 };
 __device__ inline Pair rebase(const Pair& x, float m, float n) {
     const float d = x.m - ref_of(m), f = exp2_(d * kLog2e);
     const float c = x.n - ref_of(n), g = exp2_(c * kLog2e);
     const float u = f * fmaf(x.s, d - c, x.u);
-    return {m, x.s * f, n, x.r * g, f > 0.f && x.s != 0.f ? u : 0.f};
+    return {m, x.s * f, n, x.r * g, f > 0.f && x.s != 0.f ? u : 0.f, x.w};
 }
 __device__ inline Pair join(const Pair& x, const Pair& y) {
     const float m = fmaxf(x.m, y.m), n = fmaxf(x.n, y.n);
     const Pair p = rebase(x, m, n), q = rebase(y, m, n);
-    return {m, p.s + q.s, n, p.r + q.r, p.u + q.u};
+    return {m, p.s + q.s, n, p.r + q.r, p.u + q.u, fmaxf(p.w, q.w)};
 }
 
 __device__ inline Soft shfl_xor(const Soft& x, int k) {
     return {__shfl_xor(x.m, k), __shfl_xor(x.s, k), __shfl_xor(x.a, k)};
 }
 __device__ inline Pair shfl_xor(const Pair& x, int k) {
-    return {__shfl_xor(x.m, k), __shfl_xor(x.s, k), __shfl_xor(x.n, k), __shfl_xor(x.r, k), __shfl_xor(x.u, k)};
+    return {__shfl_xor(x.m, k), __shfl_xor(x.s, k), __shfl_xor(x.n, k), __shfl_xor(x.r, k), __shfl_xor(x.u, k),
+            __shfl_xor(x.w, k)};
 }
 // Joined over the workgroup, in a fixed order; every thread gets the result.
 template <typename S>
@@ -652,7 +653,7 @@ __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, 
         y[u] = Q.template from<ONCE, ALIGNED>(begin + u * kThreads + (int)threadIdx.x);
     }
     for (int base = begin; base < P.nvec; base += kSteps * kThreads) {
-        float p[kSteps][kVec], q[kSteps][kVec], m = -INFINITY, n = -INFINITY;
+        float p[kSteps][kVec], q[kSteps][kVec], m = -INFINITY, n = -INFINITY, least = INFINITY;
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
             const int i = base + u * kThreads + (int)threadIdx.x, e = P.first(i);
@@ -667,7 +668,14 @@ __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, 
             for (int j = 0; j < kVec; ++j) {
                 m = fmaxf(m, p[u][j]);
                 n = fmaxf(n, q[u][j]);
+                least = fminf(least, q[u][j]);
             }
+        if (least == -INFINITY) {
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) st.w = fmaxf(st.w, q[u][j] == -INFINITY ? p[u][j] : -INFINITY);
+        }
         st = rebase(st, fmaxf(st.m, m), fmaxf(st.n, n));
         const float mr = ref_of(st.m), nr = ref_of(st.n);
 #pragma unroll
@@ -683,6 +691,8 @@ __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, 
     }
 }
 
+constexpr float kLeastLog = -745.f;  // e^-745 is the smallest positive double
+
 template <typename T, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
     const int r = blockIdx.x / a.parts, part = blockIdx.x % a.parts, t = threadIdx.x;
@@ -696,7 +706,7 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
     const int b = r / a.K, k = r % a.K, begin = part * a.chunk;
     const Row<T> P(static_cast<const T*>(a.target) + ((size_t)b * a.Kt + k) * a.V, a.V, begin + a.chunk);
     const Beside<T> Q(static_cast<const T*>(a.draft) + (size_t)r * a.V, a.V, P);
-    Pair st{-INFINITY, 0.f, -INFINITY, 0.f, 0.f};
+    Pair st{-INFINITY, 0.f, -INFINITY, 0.f, 0.f, -INFINITY};
     if (Q.aligned())
         kl_sweep<T, ONCE, true>(P, Q, begin, st);
     else
@@ -707,22 +717,25 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
         if (t == 0) {
             publish(rec, two(st.m, st.s));
             publish(rec + 1, two(st.n, st.r));
-            publish(rec + 2, two(st.u, 0.f));
+            publish(rec + 2, two(st.u, st.w));
         }
         if (!last_to_come(a.counters + r, a.parts)) return;
         rec = a.records + (size_t)r * a.parts * 3;
-        st = {-INFINITY, 0.f, -INFINITY, 0.f, 0.f};
+        st = {-INFINITY, 0.f, -INFINITY, 0.f, 0.f, -INFINITY};
         if (t < a.parts) {
             const uint64_t w0 = published(rec + t * 3), w1 = published(rec + t * 3 + 1), w2 = published(rec + t * 3 + 2);
-            st = {low(w0), high(w0), low(w1), high(w1), low(w2)};
+            st = {low(w0), high(w0), low(w1), high(w1), low(w2), high(w2)};
         }
         st = join_group(st);
         for (int i = t; i < a.parts * 3; i += kThreads) rec[i] = 0;
     }
     if (t == 0) {
         const float ls = logf(st.s), lr = logf(st.r);
-        // an empty target row says nothing; an empty draft row is infinitely far
-        a.kl[r] = st.s == 0.f ? 0.f : st.r == 0.f ? INFINITY : st.u / st.s - ls + lr;
+        // an empty target row says nothing; an empty draft row is infinitely
+        // far, and so is a token that the draft excludes and the target does
+        // not: p is positive as a double, also where e^(l - m) is 0 as a float
+        const bool excluded = (st.w - st.m) - ls > kLeastLog;
+        a.kl[r] = st.s == 0.f ? 0.f : st.r == 0.f || excluded ? INFINITY : st.u / st.s - ls + lr;
         if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(ref_of(st.m), ls, ref_of(st.n), lr);
     }
 }

@@ -538,7 +538,11 @@ spec_status spec_token_logprobs_grad(const void *logits, spec_dtype dtype, const
  * softmax(draft row k).  target_rows is the target's rows per request, K, or
  * K + 1 where the bonus row is in place (any number >= K).  Rows with mask 0
  * are not read and give 0, with a gradient of 0; so does a target row of
- * -inf alone.  q = 0 where p > 0 gives +inf.
+ * -inf alone.  A draft logit of -inf where p > 0 gives +inf; p counts as
+ * positive down to e^-745, where it is 0 as a double too, so that a target
+ * masked with large negative values and a draft masked with -inf stay finite.
+ * Beside finite draft logits, tokens of p below 2^-126 of the row's largest
+ * add nothing.
  *
  *   target_logits [B][target_rows][V], draft_logits [B][K][V], same dtype
  *   mask          [B][K] bytes, or NULL (every row counts)

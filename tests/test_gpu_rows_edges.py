@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import draft_verification_row_amd as sv
-from test_gpu_rows import DT, Ref, close, half, rows_of, tokens_of
+from test_gpu_rows import DT, Ref, check_kl, close, half, pair, rows_of, tokens_of
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,40 @@ def test_nan_rows_have_nan_gradients(dtype):
     r = sv.spec_token_logprobs(X, tokens_of(3, 4000, 5))
     g, = torch.autograd.grad((r.logprob + 3 * r.entropy).sum(), [X])
     assert g[1].isnan().all() and g[0].isfinite().all() and g[2].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gap", [60, 100, 500, 704, 800, 1024])
+@pytest.mark.parametrize("V", [40, 20000, 128256])
+def test_kl_of_an_excluded_unlikely_token(V, gap, dtype):
+    """A draft's -inf on a token that lies `gap` nats under the target's
+    largest, first, in the middle and last of the row, alone there and among
+    others as unlikely: infinite while the target's p is positive as a
+    double."""
+    T, D = (t.clone() for t in pair(1, 6, 6, V, DT[dtype], 3))
+    top = T.float().amax(-1)
+    for k, at in enumerate((0, V // 2, V - 1)):
+        T[0, k, at] = top[0, k] - gap
+        D[0, k, at] = -math.inf
+    for k, part in ((3, slice(0, V // 2)), (4, slice(V // 4, V - 2))):
+        T[0, k, part] = T[0, k].float().amax() - gap  # the part's own largest
+        T[0, k, V - 1] = T[0, k].float().amax() + gap
+        D[0, k, V // 4 + 1] = -math.inf
+    T[0, 5, 3] = torch.finfo(DT[dtype]).min  # the usual masks of either side
+    D[0, 5, 3] = -math.inf
+    kl, _ = check_kl(T, D)
+    assert kl[0, 5].isfinite()
+    assert (kl[0, :3] == math.inf).all() if gap < 740 else kl[0, :3].isfinite().all()
+
+
+def test_kl_infinities_of_split_and_unsplit_rows():
+    """The same rows one at a time, split over workgroups, and 600 at once."""
+    V = 32000
+    T, D = (t.clone() for t in pair(1, 600, 600, V, torch.bfloat16, 5))
+    T[0, :, 17] = -120.0
+    D[0, ::2, 17] = -math.inf
+    kl = sv.spec_draft_kl(T, D)
+    assert (kl[0, ::2] == math.inf).all() and kl[0, 1::2].isfinite().all()
+    for k in (0, 1, 598, 599):
+        one = sv.spec_draft_kl(T[:, k:k + 1].contiguous(), D[:, k:k + 1].contiguous())
+        assert torch.isposinf(one[0, 0]) == torch.isposinf(kl[0, k])
