@@ -9,7 +9,7 @@
 //   d log p_x / d l_j = [j = x] - p_j
 //   dH / d l_j        = -p_j (ln p_j + H)
 // and for a target row l and a draft row d with maxima m, n and sums S, R:
-//   KL = U / S - ln S + ln R,  U = sum e^(l_j - m) ((l_j - m) - (d_j - n))
+//   KL = U / S + ln(R / S),  U = sum e^(l_j - m) ((l_j - m) - (d_j - n))
 //   dKL / d d_j = q_j - p_j.
 // Differences are taken before they are scaled to base 2, so rows of the
 // type's lowest value stay finite, and a row's constant offset cancels
@@ -227,7 +227,7 @@ struct LpArgs {
     int32_t* top_tokens;
     float* top_logprob;
     int32_t* status;
-    float* stats;  // [rows][4]: max, ln of the sum, entropy, 1 where the row counts
+    float* stats;  // [rows][4]: max, ln of the sum, entropy, 1 / sum or 0 where the row does not count
     int parts, chunk;  // workgroups per row, and blocks each reads
     uint32_t* counters;
     uint64_t* records;
@@ -355,7 +355,7 @@ __device__ inline void lp_finish(const LpArgs& a, int r, int x, const T* row, co
         a.logprob[r] = some ? (widen(row[x]) - ref) - ls : -INFINITY;
         a.entropy[r] = H;
         a.status[r] = 0;
-        if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(ref, ls, H, some ? 1.f : 0.f);
+        if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(ref, ls, H, some ? 1.f / st.s : 0.f);
     }
     if (t < a.top_n) {
         const bool is = t < count && best[t] > kKeyNone;
@@ -451,14 +451,19 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
             for (int j = 0; j < kVec; ++j) m = fmaxf(m, v[u][j]);
         st = rebase(st, fmaxf(st.m, m));
         const float ref = ref_of(st.m);
+        // a tile's own sums first: a row's sum is then no long chain of small
+        // terms added to a large one
+        float s = 0.f, sd = 0.f;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float d = v[u][j] - ref, f = exp2_(d * kLog2e);
-                st.s += f;
-                st.a = fmaf(f, fmaxf(d, -3.0e38f), st.a);
+                s += f;
+                sd = fmaf(f, fmaxf(d, -3.0e38f), sd);
             }
+        st.s += s;
+        st.a += sd;
         if constexpr (TOP) {
             uint32_t order;
             if (count < a.top_n) {
@@ -599,7 +604,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
     const int x = a.tokens[r];
     const float* s = a.stats + (size_t)r * 4;
     const bool live = x >= 0 && x < a.V && s[3] != 0.f;
-    const float ref = s[0], ls = s[1], H = s[2];
+    const float ref = s[0], ls = s[1], H = s[2], inv = s[3];
     const float gl = a.g_logprob ? a.g_logprob[r] : 0.f, ge = a.g_entropy ? a.g_entropy[r] : 0.f;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -610,9 +615,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_grad(LpGradArgs a) {
             R.unpack(R.template raw<ONCE>(i), R.first(i), v);
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                const float lp = (v[j] - ref) - ls, p = exp2_(lp * kLog2e);
-                // p first: it bounds what lp + H and any weight can grow to
-                float g = p == 0.f ? 0.f : -fmaf(ge, p * (lp + H), gl * p);
+                // p from the difference itself: ln S would bring its own
+                // rounding and the difference's with it into the exponent
+                const float d = v[j] - ref, p = exp2_(d * kLog2e) * inv;
+                // p first: it bounds what ln p + H and any weight can grow to
+                float g = p == 0.f ? 0.f : -fmaf(ge, p * ((d - ls) + H), gl * p);
                 if (R.first(i) + j == x) g += gl;
                 v[j] = g;
             }
@@ -630,7 +637,7 @@ struct KlArgs {
     const uint8_t* mask;  // [B][K], or null: every row counts
     int K, Kt, V, tiles;  // target rows per request: Kt >= K
     float* kl;
-    float* stats;  // [B*K][4]: max and ln of the sum, target then draft
+    float* stats;  // [B*K][4]: max and 1 / sum or 0 for an empty row, target then draft
     const float* g_kl;
     void* grad;
     int parts, chunk;  // as in LpArgs
@@ -678,16 +685,20 @@ __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, 
         }
         st = rebase(st, fmaxf(st.m, m), fmaxf(st.n, n));
         const float mr = ref_of(st.m), nr = ref_of(st.n);
+        float s = 0.f, r = 0.f, gap = 0.f;  // a tile's own sums first
 #pragma unroll
         for (int u = 0; u < kSteps; ++u)
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
                 const float d = p[u][j] - mr, c = q[u][j] - nr;
                 const float f = exp2_(d * kLog2e), g = exp2_(c * kLog2e);
-                st.s += f;
-                st.r += g;
-                st.u += f > 0.f ? f * (d - c) : 0.f;
+                s += f;
+                r += g;
+                gap += f > 0.f ? f * (d - c) : 0.f;
             }
+        st.s += s;
+        st.r += r;
+        st.u += gap;
     }
 }
 
@@ -730,13 +741,15 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
         for (int i = t; i < a.parts * 3; i += kThreads) rec[i] = 0;
     }
     if (t == 0) {
-        const float ls = logf(st.s), lr = logf(st.r);
+        // one logarithm of the quotient: two would each bring their rounding
+        const float ls = logf(st.s), gap = logf(st.r / st.s);
         // an empty target row says nothing; an empty draft row is infinitely
         // far, and so is a token that the draft excludes and the target does
         // not: p is positive as a double, also where e^(l - m) is 0 as a float
         const bool excluded = (st.w - st.m) - ls > kLeastLog;
-        a.kl[r] = st.s == 0.f ? 0.f : st.r == 0.f || excluded ? INFINITY : st.u / st.s - ls + lr;
-        if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(ref_of(st.m), ls, ref_of(st.n), lr);
+        a.kl[r] = st.s == 0.f ? 0.f : st.r == 0.f || excluded ? INFINITY : st.u / st.s + gap;
+        if (a.stats) *reinterpret_cast<float4*>(a.stats + (size_t)r * 4) = make_float4(ref_of(st.m), st.s == 0.f ? 0.f : 1.f / st.s,
+                                                                                     ref_of(st.n), st.r == 0.f ? 0.f : 1.f / st.r);
     }
 }
 
@@ -762,7 +775,7 @@ __device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Besi
         D.unpack(y[u], D.first(i), p);
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
-            q[j] = g * (exp2_(((q[j] - s.z) - s.w) * kLog2e) - exp2_(((p[j] - s.x) - s.y) * kLog2e));
+            q[j] = g * (exp2_((q[j] - s.z) * kLog2e) * s.w - exp2_((p[j] - s.x) * kLog2e) * s.y);
         store_block<ONCE>(out, D, i, whole, q);
     }
 }
@@ -777,7 +790,7 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl_grad(KlArgs a) {
     const Row<T> D(drow, a.V);
     const bool whole = (((uintptr_t)drow ^ (uintptr_t)out) & 15) == 0;
     const float4 s = *reinterpret_cast<const float4*>(a.stats + (size_t)r * 4);
-    if ((a.mask && !a.mask[r]) || s.y == -INFINITY || s.w == -INFINITY) {  // nothing to learn from
+    if ((a.mask && !a.mask[r]) || s.y == 0.f || s.w == 0.f) {  // nothing to learn from
         const float zero[kVec] = {};
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {

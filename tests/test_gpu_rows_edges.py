@@ -99,3 +99,50 @@ def test_kl_infinities_of_split_and_unsplit_rows():
     for k in (0, 1, 598, 599):
         one = sv.spec_draft_kl(T[:, k:k + 1].contiguous(), D[:, k:k + 1].contiguous())
         assert torch.isposinf(one[0, 0]) == torch.isposinf(kl[0, k])
+
+
+# Rows of n equal maxima, whose sum is exactly n, with tokens d = -16 .. -20
+# under them (multiples of 2^-6, so that d is exact), which add less than
+# 2^-26 of it.  p = 2^(d log2 e) / n then has these errors: the product's
+# rounding, half a step of [16, 32) times ln 2, 11.1 u; log2 e's own, 1.34e-8
+# |d|, 4.5 u at -20; the exponential's step, 2 u; 1 / n and the last product,
+# u each; the sum's, below u.
+P_TOL = 21 * 2.0 ** -24
+
+
+def flat_rows(rows, V, n, seed):
+    at = torch.randperm(V, generator=torch.Generator().manual_seed(seed)).cuda()
+    d = -16.0 - torch.arange(256, device="cuda") / 64
+    X = torch.full((rows, V), -math.inf, device="cuda")
+    X[:, at[:n]] = 3.0
+    X[:, at[n:n + 256]] = 3.0 + d
+    return X, at[n:n + 256], torch.exp(d.double()) / (n + torch.exp(d.double()).sum())
+
+
+@pytest.mark.parametrize("n", [1000, 3001, 4095])
+@pytest.mark.parametrize("rows", [1, 600])
+def test_gradients_of_unlikely_tokens_are_good_to_their_exponent(rows, n):
+    V = 8192
+    X, at, p = flat_rows(rows, V, n, n)
+    tok = torch.full((rows,), int((X[0] == 3.0).nonzero()[0]), dtype=torch.int32, device="cuda")
+    X.requires_grad_()
+    g, = torch.autograd.grad(sv.spec_token_logprobs(X, tok).logprob.sum(), [X])
+    assert ((-g[:, at].double() - p).abs() <= P_TOL * p).all()
+    T = torch.full((1, rows, V), -math.inf, device="cuda")
+    T[:, :, tok[0]] = 1.0
+    gd, = torch.autograd.grad(sv.spec_draft_kl(T, X[None]).sum(), [X])
+    assert ((gd[:, at].double() - p).abs() <= P_TOL * p).all()
+
+
+@pytest.mark.parametrize("rows", [1, 600])
+@pytest.mark.parametrize("n,more", [(1000, 24), (3000, 1), (4000, 96), (1, 1), (7, 4000)])
+def test_kl_of_flat_rows_is_good_to_its_quotient(rows, n, more):
+    """Uniform over n tokens against uniform over n + more: ln(1 + more / n),
+    off by the quotient's half step and the logarithm's own steps."""
+    V = 8192
+    T, D = torch.full((2, 1, rows, V), -math.inf, device="cuda")
+    D[..., 50:50 + n + more] = -2.0
+    T[..., 51:51 + n] = 5.0
+    want = math.log1p(more / n)
+    kl = sv.spec_draft_kl(T, D).double()
+    assert ((kl - want).abs() <= 2.0 ** -24 * (1 + 4 * want)).all()
