@@ -817,7 +817,7 @@ inline int tiles_of(spec_dtype d, int V) {
 }
 // One workgroup per tile, in a launch of fewer than 2^32 threads.
 inline bool rows_ok(spec_dtype d, long long rows, int V) {
-    return rows >= 1 && V >= 1 && V <= SPEC_MAX_V && rows * tiles_of(d, V) < (1ll << 24);
+    return rows >= 1 && rows < (1ll << 24) && V >= 1 && V <= SPEC_MAX_V && rows * tiles_of(d, V) < (1ll << 24);
 }
 inline bool ws_ok(const void* p, size_t bytes, size_t need) {
     return p && (uintptr_t)p % 256 == 0 && bytes >= need;
