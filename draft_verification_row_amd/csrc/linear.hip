@@ -14,6 +14,7 @@
 #include <math.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <type_traits>
 #include <utility>
@@ -723,7 +724,16 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_bias_sum(const float* part, 
 }
 
 // ---------------------------------------------------------------- host side
-inline bool types_ok(spec_dtype d, spec_dtype o) {
+// An enum's value from its bytes: a caller may have put any number there.
+template <typename E>
+inline int value_of(const E& e) {
+    static_assert(sizeof(E) == sizeof(int), "enums of the ABI are ints");
+    int v;
+    memcpy(&v, &e, sizeof v);
+    return v;
+}
+inline bool types_ok(const spec_dtype& dtype, const spec_dtype& out_dtype) {
+    const int d = value_of(dtype), o = value_of(out_dtype);
     return d == SPEC_BF16 ? (o == SPEC_BF16 || o == SPEC_F32) : d == SPEC_F32 && o == SPEC_F32;
 }
 constexpr long long kMaxElems = 1ll << 34;  // of a matrix: launches stay below 2^32 threads
@@ -731,7 +741,7 @@ inline bool sizes_ok(long long M, long long N, long long K) {
     return M >= 1 && N >= 1 && K >= 1 && M <= SPEC_MAX_LINEAR && N <= SPEC_MAX_LINEAR && K <= SPEC_MAX_LINEAR &&
            M * N < kMaxElems && M * K < kMaxElems && N * K < kMaxElems;
 }
-inline bool act_ok(int a) { return a >= SPEC_ACT_NONE && a <= SPEC_ACT_SILU; }
+inline bool act_ok(const spec_activation& a) { return value_of(a) >= SPEC_ACT_NONE && value_of(a) <= SPEC_ACT_SILU; }
 inline size_t elem(spec_dtype d) { return d == SPEC_BF16 ? 2 : 4; }
 inline bool ws_ok(const void* p, size_t bytes, size_t need) {
     return p && (uintptr_t)p % 256 == 0 && bytes >= need;

@@ -20,6 +20,7 @@
 #include <math.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "spec_verify.h"
 
@@ -808,7 +809,15 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl_grad(KlArgs a) {
 }
 
 // ---------------------------------------------------------------- host side
-inline bool dtype_ok(spec_dtype d) { return d == SPEC_F32 || d == SPEC_BF16; }
+// An enum's value from its bytes: a caller may have put any number there.
+template <typename E>
+inline int value_of(const E& e) {
+    static_assert(sizeof(E) == sizeof(int), "enums of the ABI are ints");
+    int v;
+    memcpy(&v, &e, sizeof v);
+    return v;
+}
+inline bool dtype_ok(const spec_dtype& d) { return value_of(d) == SPEC_F32 || value_of(d) == SPEC_BF16; }
 
 // Tiles of a row at any alignment.
 inline int tiles_of(spec_dtype d, int V) {

@@ -57,16 +57,20 @@ int main() {
     expect("lp null", spec_token_logprobs(nullptr, SPEC_BF16, I, 4, 100, 0, F, F, nullptr, nullptr, I, nullptr, W, all, nullptr), SPEC_EINVAL);
     expect("lp top null", spec_token_logprobs(P, SPEC_BF16, I, 4, 100, 3, F, F, nullptr, F, I, nullptr, W, all, nullptr), SPEC_EINVAL);
     expect("lp stats", spec_token_logprobs(P, SPEC_BF16, I, 4, 100, 0, F, F, nullptr, nullptr, I, G, W, all, nullptr), SPEC_EINVAL);
+    expect("lp dtype", spec_token_logprobs(P, (spec_dtype)2, I, 4, 100, 0, F, F, nullptr, nullptr, I, nullptr, W, all, nullptr), SPEC_EDTYPE);
+    expect("lp grad dtype", spec_token_logprobs_grad(P, (spec_dtype)7, I, F, F, F, 4, 100, P, nullptr), SPEC_EDTYPE);
     expect("lp grad stats", spec_token_logprobs_grad(P, SPEC_F32, I, G, F, F, 4, 100, P, nullptr), SPEC_EINVAL);
     expect("lp grad rows", spec_token_logprobs_grad(P, SPEC_F32, I, F, F, F, INT_MAX, 262144, P, nullptr), SPEC_EINVAL);
     expect("lp grad out", spec_token_logprobs_grad(P, SPEC_F32, I, F, F, F, 4, 100, nullptr, nullptr), SPEC_EINVAL);
     // divergence
     expect("kl rows", spec_draft_kl(P, P, SPEC_BF16, nullptr, 2, 3, 2, 100, F, nullptr, W, all, nullptr), SPEC_EINVAL);
     expect("kl target rows", spec_draft_kl(P, P, SPEC_BF16, nullptr, 65536, 1, INT_MAX, 100, F, nullptr, W, all, nullptr), SPEC_EINVAL);
+    expect("kl dtype", spec_draft_kl(P, P, (spec_dtype)3, nullptr, 2, 3, 3, 100, F, nullptr, W, all, nullptr), SPEC_EDTYPE);
     expect("kl grad null", spec_draft_kl_grad(P, P, SPEC_BF16, nullptr, F, nullptr, 2, 3, 3, 100, P, nullptr), SPEC_EINVAL);
     expect("kl grad stats", spec_draft_kl_grad(P, P, SPEC_BF16, nullptr, G, F, 2, 3, 3, 100, P, nullptr), SPEC_EINVAL);
     // product
     expect("linear types", spec_linear(P, P, nullptr, nullptr, SPEC_F32, SPEC_BF16, SPEC_ACT_NONE, 4, 8, 16, P, nullptr, W, all, nullptr), SPEC_EDTYPE);
+    expect("linear act", spec_linear(P, P, nullptr, nullptr, SPEC_F32, SPEC_F32, (spec_activation)4, 4, 8, 16, P, nullptr, W, all, nullptr), SPEC_EINVAL);
     expect("linear grad preact", spec_linear_grad(P, P, nullptr, P, SPEC_F32, SPEC_F32, SPEC_ACT_SILU, 4, 8, 16, P, P, P, W, all, nullptr), SPEC_EINVAL);
     expect("linear grad x", spec_linear_grad(nullptr, P, P, P, SPEC_F32, SPEC_F32, SPEC_ACT_SILU, 4, 8, 16, P, P, P, W, all, nullptr), SPEC_EINVAL);
 
