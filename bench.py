@@ -229,8 +229,10 @@ class Case:
             if rc != 0:
                 raise RuntimeError(f"{self.mode} call failed with status {rc}")
 
-    def snapshot(self):
-        return [{k: v.clone() for k, v in o.items()} for o in self.outputs]
+    def snapshot(self, steps):
+        """Copies of the outputs that `steps` calls have written: with fewer
+        steps than input sets the other sets' outputs were never written."""
+        return [{k: v.clone() for k, v in o.items()} for o in self.outputs[:steps]]
 
 
 def time_case(case, steps, warmup, hip, use_graph):
@@ -248,7 +250,7 @@ def time_case(case, steps, warmup, hip, use_graph):
     hip.lib.hipEventRecord(b, ctypes.c_void_p(stream))
     torch.cuda.synchronize()
     res["eager_ms_per_step"] = hip.elapsed_ms(a, b) / steps
-    eager_out = case.snapshot()
+    eager_out = case.snapshot(steps)
     res["outputs"] = eager_out
     # graph replay of exactly `steps` calls
     if use_graph:
@@ -272,7 +274,7 @@ def time_case(case, steps, warmup, hip, use_graph):
         res["graph_ms_per_step"] = sorted(runs)[len(runs) // 2]
         res["graph_ms_per_step_runs"] = runs
         # the timed replays must reproduce the eager results bit for bit
-        res["outputs"] = case.snapshot()
+        res["outputs"] = case.snapshot(steps)
         for o1, o2 in zip(eager_out, res["outputs"]):
             for k in o1:
                 if not torch.equal(o1[k], o2[k]):
