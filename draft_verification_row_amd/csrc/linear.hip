@@ -186,9 +186,10 @@ __device__ inline bool four_at_once(const Gemm& g) {
 }
 
 // -------------------------------------------------------------- tiled product
-// Bound by the matrix cores: 4096 x 4096 x 8192 bf16 219 us (1255 TFLOP/s), of
-// which the instructions themselves are busy about two thirds; fp32 1835 us
-// (150 TFLOP/s).
+// Bound by the matrix cores: 4096 x 4096 x 8192 bf16 203 us (1354 TFLOP/s), of
+// which the instructions themselves are busy about two thirds; fp32 1836 us
+// (150 TFLOP/s); 8192 x 4096 x 4096 bf16, with half of the steps to each
+// epilogue, 232 us.
 // BM x BN outputs per workgroup of four waves; a wave has WM x WN of them in
 // 32 x 32 blocks, weights as the instruction's first operand, so that a lane
 // ends with four neighbouring n of one m.  The rows'
@@ -211,7 +212,9 @@ __device__ inline void tile_of(int id, int count, int tiles_m, int tiles_n, int&
 }
 
 // 16 bytes a lane from the buffer straight to LDS at base + AT + lane * 16.
-// NT: read once, not to be kept in the caches.
+// NT: read once, not to be kept in the caches.  m0 cannot be listed as
+// clobbered (the compiler reserves it); it is free, since nothing else in these
+// kernels uses it.
 template <int AT, bool NT>
 __device__ inline void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t base, uint32_t voffset, uint32_t soffset) {
     if constexpr (NT)
@@ -516,8 +519,9 @@ __global__ __launch_bounds__(kThreads) void k_finish(Gemm g) {
 // waves take every fourth piece of 256 bytes of the rows, W and X
 // straight into registers as operands of 16x16 instructions (lane l: row
 // l % 16, chunk l / 16), the next piece on its way while one is multiplied.
-// The waves' sums are added in LDS.  One row of 4096 x 4096: bf16 10 us, of
-// which about 5 are the launch, fp32 25 us.
+// The waves' sums are added in LDS.  One row of 4096 x 4096: bf16 11.7 us, of
+// which about 5 are the launch, fp32 24 us; one row of 512 x 8192, where 32
+// workgroups leave most of the chip idle, 15 and 32 us.
 __device__ inline f32x4 mfma16(bf16, u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
@@ -754,11 +758,12 @@ inline spec_status launched() { return hipGetLastError() == hipSuccess ? SPEC_OK
 // by 128 of W, which keep more of W on its way (us at N 128256, K 4096, bf16:
 // one row 155, k_few 199; 32 rows 169, 187 with temporal loads).  Else the
 // largest tile that still gives kEnough workgroups: 256 (4096 x 4096 x 8192
-// bf16: 219 us; 128: 259), 128 (1024 x 4096 x 4096: 34 us), 64; and where 64
-// leaves compute units idle, K is split over several workgroups a tile, of at
-// least four steps each, their fp32 sums added by one more launch, where the
-// steps saved outweigh that launch (split / not, us: 512 x 512 x 8192 bf16
-// 18.6 / 26.6, fp32 45.8 / 140.8; 192 x 4096 x 4096 bf16 19.8 / 15.8).
+// bf16: 219 us beside 259 with 128, timed together), 128 (1024 x 4096 x 4096:
+// 37 us), 64; and where 64 leaves compute units idle, K is split over several
+// workgroups a tile, of at least four steps each, their fp32 sums added by one
+// more launch, where the steps saved outweigh that launch (split / not, us:
+// 512 x 512 x 8192 bf16 18.6 / 26.6, fp32 45.8 / 140.8; 192 x 4096 x 4096 bf16
+// 19.8 / 15.8).
 constexpr int kWide = 16384, kEnough = 200, kSplitGroups = 512, kMaxSplits = 8, kSplitWorth = 50;
 enum Choice { kFew, kRows32, kRows64, kTile256, kTile128, kTile64 };
 inline long long tiles_of(long long M, long long N, int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); }
@@ -792,8 +797,13 @@ inline size_t split_bytes(spec_dtype d, long long M, long long N, long long K) {
 // A K that is no whole number of chunks leaves rows that cannot be loaded
 // directly.  For the larger tiles both operands are copied to padded rows
 // first, which costs their bytes once; the smaller ones load through registers
-// (copied / not, us: 4096 x 4096 x 4095 bf16 172 / 384, fp32 1005 / 1220,
-// 1500 x 2000 x 777 bf16 20.2 / 20.7).
+// (copied / not, us: 4096 x 4096 x 4095 bf16 156 / 355, fp32 991 / 1222,
+// 1500 x 2000 x 777 bf16 20.3 / 20.3).  Two kinds of operands are not copied
+// and load through registers whatever the size, into tiles of 64: up to 64
+// rows over a wide W of odd K, where the copy would move W twice more (32 x
+// 128256 x 4095 bf16 311 us, K 4096 170), and operands off 16-byte alignment,
+// which the workspace's size cannot tell (4096 x 4096 x 4096 bf16 119 us, x off
+// by an element 330, W too 463; fp32 932 and 1230).
 inline bool packs(spec_dtype d, long long M, long long N, long long K) {
     const Choice c = choose(M, N);
     return K * (long long)elem(d) % 16 != 0 && (c == kTile256 || c == kTile128);

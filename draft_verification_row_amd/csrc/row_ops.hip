@@ -379,8 +379,8 @@ __device__ inline float high(uint64_t w) { return __uint_as_float((uint32_t)(w >
 // the others published before is then visible, since published words are
 // written and read with agent-scope atomics, past the XCDs' caches, and have
 // arrived before the counter is raised (a release fence would write back and
-// invalidate the whole XCD's cache: 47 us instead of 27 for the divergence of
-// 160 rows of 128256).  The last one leaves the counter at zero.
+// invalidate the whole XCD's cache: 47 us beside 27 for the divergence of 160
+// rows of 128256, timed together).  The last one leaves the counter at zero.
 __device__ inline bool last_to_come(uint32_t* counter, int parts) {
     __shared__ int last;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -403,12 +403,12 @@ __device__ inline bool last_to_come(uint32_t* counter, int parts) {
 // logits above the last one kept (their indices are higher, so a tie loses).
 // U: blocks per thread and tile.  The next tile is loaded while one is worked
 // on.
-// Bound by reading where there are many rows: 1844 rows of 151936 bf16 take 94
-// us (6.0 TB/s); 2048 rows through the caches 110 us, and 160 us with 20
-// alternatives, whose scan for candidates costs about as many instructions as
-// the statistics.  144 rows of 128256 take
-// 14 us (2.6 TB/s), 25 us with 20; six rows 7.5 and 12.5 us: there it is the
-// launch, the join and the fold, one after the other.
+// Bound by reading where there are many rows: 2048 rows of 151936 bf16 take
+// 111 us (median; 5.6 TB/s), and 183 us with 20 alternatives, whose scan for
+// candidates costs about as many instructions as the statistics.  144 rows of
+// 128256 take 15 us (2.5 TB/s), 25 us with 20; with 48 padded rows among them,
+// which take their share of the split, 31 us; six rows 7.8 us, and 11.3 us
+// with 5: there it is the launch, the join and the fold, one after the other.
 template <typename T, bool TOP, int U, bool ONCE>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LpArgs a) {
     constexpr int kVec = Row<T>::kVec;
@@ -648,8 +648,9 @@ struct KlArgs {
 
 // Split over workgroups like k_logprobs.  Blocks follow the target's row.
 // Bound by reading both rows and, close behind, by two exponentials a token:
-// 177 us for 1844 rows of 128255 bf16 (5.3 TB/s), 205 through the caches; 23 us
-// for 128 of 128256.
+// 187 us for 2048 rows of 128255 bf16 (median; 5.6 TB/s), 216 us with a tenth
+// of them masked in between; 19.5 us for 128 rows of 128256, 24 us with 32
+// masked ones among them, which take their share of the split.
 template <typename T, bool ONCE, bool ALIGNED>
 __device__ inline void kl_sweep(const Row<T>& P, const Beside<T>& Q, int begin, Pair& st) {
     constexpr int kVec = Row<T>::kVec;
@@ -755,8 +756,8 @@ __global__ __launch_bounds__(kThreads) void k_draft_kl(KlArgs a) {
 }
 
 // One workgroup per tile of a draft row: reads both rows, writes the gradient,
-// bound by that: forward and gradient of 2048 rows of 128255 bf16, a tenth of
-// them masked, take 454 us for 2.4 GB (5.3 TB/s).
+// bound by that: 2048 rows of 128255 bf16 take 269 us (median) for 1.58 GB (5.9
+// TB/s), 262 us with a tenth of them masked.
 template <typename T, bool ONCE, bool ALIGNED>
 __device__ inline void kl_grad_tile(const KlArgs& a, const Row<T>& D, const Beside<T>& P, T* out, bool whole, int tile, const float4& s, float g) {
     constexpr int kVec = Row<T>::kVec;
