@@ -20,6 +20,7 @@ __all__ = ["spec_verify_greedy", "spec_verify_exact", "spec_verify_relaxed", "sp
            "spec_verify_power", "spec_sample_drafts", "spec_verify_workspace_bytes", "spec_sample_workspace_bytes",
            "VerifyResult", "TreeResult", "SampleResult", "SpecVerifyError",
            "spec_token_logprobs", "spec_draft_kl", "spec_linear", "LogprobResult", "SPEC_MAX_TOP",
+           "spec_embedding", "spec_gated_linear", "spec_cross_entropy", "CrossEntropyResult",
            "library_path", "load_library", "spec_set_spin_limit", "SPEC_MAX_K", "SPEC_MAX_NODES"]
 
 SPEC_F32, SPEC_BF16 = 0, 1
@@ -91,7 +92,12 @@ def load_library():
     lib.spec_set_spin_limit.argtypes = [I]
     lib.spec_set_spin_limit.restype = None
     for fn, n in (("spec_logprobs_workspace_bytes", 4), ("spec_draft_kl_workspace_bytes", 4),
-                  ("spec_linear_workspace_bytes", 4), ("spec_linear_grad_workspace_bytes", 4)):
+                  ("spec_linear_workspace_bytes", 4), ("spec_linear_grad_workspace_bytes", 4),
+                  ("spec_embedding_grad_workspace_bytes", 4),
+                  ("spec_gated_linear_workspace_bytes", 4),
+                  ("spec_gated_linear_grad_workspace_bytes", 4),
+                  ("spec_cross_entropy_workspace_bytes", 4),
+                  ("spec_cross_entropy_grad_workspace_bytes", 4)):
         getattr(lib, fn).argtypes = [I] * n
         getattr(lib, fn).restype = Z
     lib.spec_token_logprobs.argtypes = [P, I, P, I, I, I, P, P, P, P, P, P, P, Z, P]
@@ -100,7 +106,15 @@ def load_library():
     lib.spec_draft_kl_grad.argtypes = [P, P, I, P, P, P, I, I, I, I, P, P]
     lib.spec_linear.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P, P, Z, P]
     lib.spec_linear_grad.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P, P, P, Z, P]
+    lib.spec_embedding.argtypes = [P, I, P, F, I, I, I, P, P]
+    lib.spec_embedding_grad.argtypes = [P, P, I, F, I, I, I, P, P, Z, P]
+    lib.spec_gated_linear.argtypes = [P, P, P, I, I, I, I, I, P, P, P, P, Z, P]
+    lib.spec_gated_linear_grad.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, Z, P]
+    lib.spec_cross_entropy.argtypes = [P, P, P, I, P, I, I, I, P, P, P, P, P, Z, P]
+    lib.spec_cross_entropy_grad.argtypes = [P, P, P, I, P, P, P, P, I, I, I, P, P, P, P, Z, P]
     for fn in ("spec_verify_greedy", "spec_verify_exact", "spec_verify_exact_noalloc",
+               "spec_embedding", "spec_embedding_grad", "spec_gated_linear",
+               "spec_gated_linear_grad", "spec_cross_entropy", "spec_cross_entropy_grad",
                "spec_token_logprobs", "spec_token_logprobs_grad", "spec_draft_kl",
                "spec_draft_kl_grad", "spec_linear", "spec_linear_grad",
                "spec_verify_relaxed", "spec_verify_tree",
@@ -366,3 +380,5 @@ def spec_verify_tree(target_logits: torch.Tensor, node_tokens: torch.Tensor,
 
 from .heads import (LogprobResult, SPEC_MAX_TOP, spec_draft_kl, spec_linear,  # noqa: E402
                     spec_token_logprobs)
+from .training import (CrossEntropyResult, spec_cross_entropy, spec_embedding,  # noqa: E402
+                       spec_gated_linear)

@@ -13,7 +13,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SRCS = [os.path.join(CSRC, f) for f in ("spec_verify.hip", "row_ops.hip", "linear.hip")]
+SRCS = [os.path.join(CSRC, f) for f in ("spec_verify.hip", "row_ops.hip", "linear.hip", "embedding.hip",
+                                           "gated.hip", "cross_entropy.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libspecverify.so")
 

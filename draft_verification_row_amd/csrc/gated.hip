@@ -1,0 +1,342 @@
+// gated.hip -- the gated block of a draft head, for gfx950 (MI355X): two
+// projections, an activation and their product, with the gradients.
+//
+//   g = x G^T, u = x U^T, y = act(g) u      x [M][K], G, U [N][K], y [M][N]
+//   dg = dy u act'(g), du = dy act(g)
+//   dx = dg G + du U, dG = dg^T x, dU = du^T x
+// Products are summed in fp32, y is formed from the fp32 sums and rounded once.
+// With bf16 operands the kept g and u and the slopes dg and du are bf16: the
+// slopes are operands of the matrix instructions, and g and u move them by
+// about as much as their own rounding does.
+#include "product.h"
+
+namespace {
+
+// ------------------------------------------------------------------- forward
+// Both matrices side by side in one tile, so that a wave ends with g and u of
+// the same outputs, x is loaded once for both and y needs no second pass.
+template <typename T>
+struct Gate : FromZero {
+    T *y, *g, *u;  // g and u: kept for the gradient, or null
+    int act;
+    bool whole;
+    template <class C>
+    __device__ __attribute__((always_inline)) void finish(const Part& p, f32x16 (&acc)[C::FN][C::FM]) const {
+        constexpr int kLanes = C::kWaveN / 4, kAtOnce = 64 / kLanes, kPitch = C::WN + 4;
+        const int c = p.lane % kLanes * 4, n = p.n0 + c;
+        turned<C>(p, acc, [&](int j, float* rows) __attribute__((always_inline)) {
+            if (n >= p.N) return;
+#pragma unroll 4
+            for (int r = p.lane / kLanes; r < 32; r += kAtOnce) {
+                const int m = p.m0 + j * 32 + r;
+                if (m >= p.M) break;
+                const f32x4 a = *reinterpret_cast<const f32x4*>(rows + r * kPitch + c);
+                const f32x4 b = *reinterpret_cast<const f32x4*>(rows + r * kPitch + C::kWaveN + c);
+                out4(m, n, p.N, a, b);
+            }
+        });
+    }
+    __device__ void out4(int m, int n, int N, f32x4 a, f32x4 b) const {
+        const float va[4] = {a[0], a[1], a[2], a[3]}, vb[4] = {b[0], b[1], b[2], b[3]};
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = act_of(va[i], act) * vb[i];
+        const int64_t at = (int64_t)m * N + n;
+        if (whole) {
+            if (g) put4(g + at, va), put4(u + at, vb);
+            put4(y + at, v);
+        } else {
+            for (int i = 0; i < 4 && n + i < N; ++i) {
+                if (g) put(g + at + i, va[i]), put(u + at + i, vb[i]);
+                put(y + at + i, v[i]);
+            }
+        }
+    }
+};
+
+// M <= 16: bound by reading G and U once.  A workgroup has 16 rows of each; its
+// four waves take every fourth piece of 256 bytes of the rows, straight into
+// registers as operands of 16x16 instructions (lane l: row l % 16, chunk l /
+// 16), the next piece on its way while one is multiplied.  The waves' sums are
+// added in LDS.
+__device__ inline f32x4 mfma16(bf16, u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ inline f32x4 mfma16(float, u32x4 a, u32x4 b, f32x4 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], c, 0, 0, 0);
+    return c;
+}
+
+template <typename T, bool ALIGNED>
+__global__ __launch_bounds__(kThreads) void k_gated_few(Product g, Gate<T> e) {
+    constexpr int kElems = 16 / (int)sizeof(T), KS = 4, kPiece = KS * 4 * kElems, kPitch = 20;
+    __shared__ float sums[4][2][16][kPitch];
+    const int t = threadIdx.x, lane = t & 63, w = t >> 6, r = lane & 15, c = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const T* G = static_cast<const T*>(g.w[0]) + min(n0 + r, g.N - 1) * g.ldw;
+    const T* U = static_cast<const T*>(g.w[1]) + min(n0 + r, g.N - 1) * g.ldw;
+    const T* X = static_cast<const T*>(g.x[0]) + min(r, g.M - 1) * g.ldx;
+    struct Piece {
+        u32x4 a[KS], b[KS], x[KS];
+    };
+    auto load = [&](int p, Piece& q) {
+        const bool full = ALIGNED && (p + 1) * kPiece <= g.K;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int k = p * kPiece + (s * 4 + c) * kElems;
+            q.a[s] = full ? *reinterpret_cast<const u32x4*>(G + k) : chunk_of(G, k, g.K);
+            q.b[s] = full ? *reinterpret_cast<const u32x4*>(U + k) : chunk_of(U, k, g.K);
+            q.x[s] = (u32x4){0, 0, 0, 0};
+            if (r < g.M) q.x[s] = full ? *reinterpret_cast<const u32x4*>(X + k) : chunk_of(X, k, g.K);
+        }
+    };
+    f32x4 acc[2] = {};
+    const int pieces = (g.K + kPiece - 1) / kPiece;
+    Piece q;
+    if (w < pieces) load(w, q);
+    for (int p = w; p < pieces; p += 4) {
+        Piece next;
+        if (p + 4 < pieces) load(p + 4, next);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            acc[0] = mfma16(T(), q.a[s], q.x[s], acc[0]);
+            acc[1] = mfma16(T(), q.b[s], q.x[s], acc[1]);
+        }
+        q = next;
+    }
+    *reinterpret_cast<f32x4*>(&sums[w][0][r][c * 4]) = acc[0];
+    *reinterpret_cast<f32x4*>(&sums[w][1][r][c * 4]) = acc[1];
+    __syncthreads();
+    if (t < 64) {
+        const int m = t / 4, n = t % 4 * 4;
+        f32x4 v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[i] = *reinterpret_cast<const f32x4*>(&sums[0][i][m][n]);
+#pragma unroll
+            for (int k = 1; k < 4; ++k) v[i] += *reinterpret_cast<const f32x4*>(&sums[k][i][m][n]);
+        }
+        if (m < g.M && n0 + n < g.N) e.out4(m, n0 + n, g.N, v[0], v[1]);
+    }
+}
+
+// The splits' sums of g and u, [splits][2][M][N], added and finished.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_gated_join(const float* part, int splits, int M, int N, Gate<T> e) {
+    const int across = (N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int m = (int)(i / across), n = (int)(i % across) * 4;
+    if (m >= M) return;
+    f32x4 v[2] = {};
+    for (int s = 0; s < splits; ++s)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float* p = part + ((int64_t)(s * 2 + k) * M + m) * N + n;
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) v[k][j] += p[j];
+        }
+    e.out4(m, n, N, v[0], v[1]);
+}
+
+// --------------------------------------------------------------- the slopes
+// dg and du from dy, g and u, rows padded to whole chunks.  Bound by memory.
+struct GateSlope {
+    const void *dy, *g, *u;
+    void *dg, *du;
+    int act, M, N;
+    int64_t ld;
+    bool whole;
+};
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_gated_slopes(GateSlope a) {
+    constexpr int kElems = 16 / (int)sizeof(T);
+    const int across = (int)(a.ld / kElems);
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int m = (int)(i / across), n = (int)(i % across) * kElems;
+    if (m >= a.M) return;
+    const int64_t at = (int64_t)m * a.N;
+    u32x4 q[3];
+    const T* from[3] = {static_cast<const T*>(a.dy) + at, static_cast<const T*>(a.g) + at, static_cast<const T*>(a.u) + at};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) q[k] = a.whole ? *reinterpret_cast<const u32x4*>(from[k] + n) : chunk_of(from[k], n, a.N);
+    float dg[kElems], du[kElems];
+#pragma unroll
+    for (int j = 0; j < kElems; ++j) {
+        float v[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            v[k] = __uint_as_float(sizeof(T) == 4 ? q[k][j % 4] : (j & 1) ? q[k][j >> 1] & 0xffff0000u : q[k][j >> 1] << 16);
+        dg[j] = v[0] * v[2] * act_slope(v[1], a.act);
+        du[j] = v[0] * act_of(v[1], a.act);
+    }
+    T* to[2] = {static_cast<T*>(a.dg) + m * a.ld + n, static_cast<T*>(a.du) + m * a.ld + n};
+#pragma unroll
+    for (int j = 0; j < kElems; j += 4) {
+        put4(to[0] + j, {dg[j], dg[j + 1], dg[j + 2], dg[j + 3]});
+        put4(to[1] + j, {du[j], du[j + 1], du[j + 2], du[j + 3]});
+    }
+}
+
+// ---------------------------------------------------------------- host side
+inline bool gated_ok(spec_dtype d, long long M, long long N, long long K) {
+    const int t = value_of(d);
+    return (t == SPEC_BF16 || t == SPEC_F32) && M >= 1 && N >= 1 && K >= 1 && M <= SPEC_MAX_LINEAR && N <= SPEC_MAX_LINEAR &&
+           K <= SPEC_MAX_LINEAR && M * N < (1ll << 33) && M * K < (1ll << 33) && N * K < (1ll << 33);
+}
+
+// Rows whose length is no whole number of chunks are copied to padded ones for
+// the larger tiles, which load straight to LDS.
+inline size_t packed_bytes(spec_dtype d, long long rows, long long k) { return align_up((size_t)(rows * padded(d, k)) * elem(d), 256); }
+inline bool packs_pair(spec_dtype d, long long M, long long N, long long K) {
+    return padded(d, K) != K && M > 16 && size_of(M, 2 * N, 1) != kTile64;
+}
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_pad_rows(const T* from, int64_t rows, int K, int64_t ld, T* to) {
+    constexpr int kElems = 16 / (int)sizeof(T);
+    const int64_t across = ld / kElems, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t m = i / across;
+    if (m >= rows) return;
+    const int k = (int)(i % across) * kElems;
+    *reinterpret_cast<u32x4*>(to + m * ld + k) = chunk_of(from + m * K, k, K);
+}
+template <typename T>
+void pad_rows(const void* from, long long rows, int K, int64_t ld, void* to, hipStream_t st) {
+    const int64_t n = rows * (ld / (16 / (int64_t)sizeof(T)));
+    k_pad_rows<T><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(static_cast<const T*>(from), rows, K, ld, static_cast<T*>(to));
+}
+
+template <typename T>
+void gated_forward(Product g, const Gate<T>& e, spec_dtype d, char* ws, hipStream_t st) {
+    if (g.M <= 16) {
+        const unsigned grid = (unsigned)((g.N + 15) / 16);
+        if (aligned(g, sizeof(T)))
+            k_gated_few<T, true><<<grid, kThreads, 0, st>>>(g, e);
+        else
+            k_gated_few<T, false><<<grid, kThreads, 0, st>>>(g, e);
+        return;
+    }
+    if (packs_pair(d, g.M, g.N, g.K)) {
+        const int64_t ld = padded(d, g.K);
+        char *x = ws, *a = x + packed_bytes(d, g.M, g.K), *b = a + packed_bytes(d, g.N, g.K);
+        pad_rows<T>(g.x[0], g.M, g.K, ld, x, st);
+        pad_rows<T>(g.w[0], g.N, g.K, ld, a, st);
+        pad_rows<T>(g.w[1], g.N, g.K, ld, b, st);
+        g.x[0] = x, g.w[0] = a, g.w[1] = b;
+        g.ldx = g.ldw = ld;
+        g.K = (int)ld;  // the padding is zero
+    }
+    const Size size = size_of(g.M, 2ll * g.N, 1);
+    if (!aligned(g, sizeof(T)))
+        launch_tile<Tile<T, 64, 128, 32, 64, 2, false, false, true, false>>(g, e, st);
+    else if (size == kTile256)
+        launch_tile<Tile<T, 256, 256, 128, 128, 2, false, false, true, true>>(g, e, st);
+    else if (size == kTile128)
+        launch_tile<Tile<T, 128, 128, 64, 64, 4, false, false, true, true>>(g, e, st);
+    else
+        launch_tile<Tile<T, 64, 128, 32, 64, 3, false, false, true, true>>(g, e, st);
+}
+
+// The gradients' workspace: dg and du, and the sums of split products.
+struct GatedLayout {
+    int64_t np;
+    size_t dg, du, sums, total;
+    int split_x, split_w;
+};
+inline GatedLayout gated_layout(spec_dtype d, long long M, long long N, long long K) {
+    GatedLayout l;
+    l.np = padded(d, N);
+    l.dg = 0;
+    l.du = align_up((size_t)(M * l.np) * elem(d), 256);
+    l.sums = 2 * l.du;
+    l.split_x = splits_at(d, M, K, 2 * N, 1);
+    l.split_w = splits_at(d, N, K, M, 2);
+    const size_t a = l.split_x > 1 ? (size_t)(l.split_x * M * K) * 4 : 0, b = l.split_w > 1 ? (size_t)(2 * l.split_w * N * K) * 4 : 0;
+    l.total = l.sums + align_up(a > b ? a : b, 256);
+    return l;
+}
+
+template <typename T>
+void gated_backward(const void* x, const void* gate, const void* up, const void* g, const void* u, const void* dy, int act,
+                    int M, int N, int K, void* gx, void* gg, void* gu, spec_dtype d, char* ws, hipStream_t st) {
+    const GatedLayout lay = gated_layout(d, M, N, K);
+    constexpr int kElems = 16 / (int)sizeof(T);
+    void *dg = ws + lay.dg, *du = ws + lay.du;
+    float* sums = reinterpret_cast<float*>(ws + lay.sums);
+    const bool whole = N % kElems == 0 && ((uintptr_t)g | (uintptr_t)u | (uintptr_t)dy) % 16 == 0;
+    const int64_t chunks = (int64_t)M * (lay.np / kElems);
+    k_gated_slopes<T><<<(unsigned)((chunks + kThreads - 1) / kThreads), kThreads, 0, st>>>({dy, g, u, dg, du, act, M, N, lay.np, whole});
+    if (gx) {
+        const Product p{{dg, du}, {gate, up}, lay.np, K, M, K, N, N, nullptr, nullptr, 1, lay.split_x};
+        if (lay.split_x > 1) {
+            launch_product<T, false, true>(p, Store<float>{{}, {sums, sums}, K, (int64_t)M * K, false, fours(sums, K, 4)}, kTile64, st);
+            k_join<T><<<four_blocks(M, K), kThreads, 0, st>>>(sums, lay.split_x, (int64_t)M * K, nullptr, M, K, static_cast<T*>(gx));
+        } else {
+            launch_product<T, false, true>(p, Store<T>{{}, {static_cast<T*>(gx), static_cast<T*>(gx)}, K, 0, false, fours(gx, K, sizeof(T))}, size_of(M, K, 1), st);
+        }
+    }
+    if (gg || gu) {
+        // both in one launch where both are asked for
+        const void *a = gg ? dg : du, *b = gu ? du : dg;
+        T *oa = static_cast<T*>(gg ? gg : gu), *ob = static_cast<T*>(gu ? gu : gg);
+        const int products = gg && gu ? 2 : 1;
+        const Product p{{a, b}, {x, x}, lay.np, K, N, K, M, 0, nullptr, nullptr, products, lay.split_w};
+        if (lay.split_w > 1) {
+            const int64_t one = (int64_t)N * K;
+            float* second = sums + lay.split_w * one;
+            launch_product<T, true, true>(p, Store<float>{{}, {sums, second}, K, one, false, fours(sums, K, 4)}, kTile64, st);
+            k_join<T><<<four_blocks(N, K), kThreads, 0, st>>>(sums, lay.split_w, one, nullptr, N, K, oa);
+            if (products == 2) k_join<T><<<four_blocks(N, K), kThreads, 0, st>>>(second, lay.split_w, one, nullptr, N, K, ob);
+        } else {
+            const bool four = fours(oa, K, sizeof(T)) && fours(ob, K, sizeof(T));
+            launch_product<T, true, true>(p, Store<T>{{}, {oa, ob}, K, 0, false, four}, size_of(N, K, 2), st);
+        }
+    }
+}
+
+}  // namespace
+
+extern "C" size_t spec_gated_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K) {
+    if (!gated_ok(dtype, M, N, K)) return 0;
+    return packs_pair(dtype, M, N, K) ? packed_bytes(dtype, M, K) + 2 * packed_bytes(dtype, N, K) : 256;
+}
+
+extern "C" spec_status spec_gated_linear(const void* x, const void* gate, const void* up, spec_dtype dtype,
+                                         spec_activation activation, int M, int N, int K, void* out, void* out_gate,
+                                         void* out_up, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!type_ok(dtype)) return SPEC_EDTYPE;
+    if (!gated_ok(dtype, M, N, K) || !act_ok(activation) || !x || !gate || !up || !out || !out_gate != !out_up) return SPEC_EINVAL;
+    if (!ws_ok(workspace, workspace_bytes, spec_gated_linear_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
+    const Product g{{x, x}, {gate, up}, K, K, M, N, K, 0, nullptr, nullptr, 1, 1};
+    const size_t four = 4 * elem(dtype);
+    const bool whole = N % 4 == 0 && ((uintptr_t)out | (uintptr_t)out_gate | (uintptr_t)out_up) % four == 0;
+    char* ws = static_cast<char*>(workspace);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    if (value_of(dtype) == SPEC_BF16)
+        gated_forward(g, Gate<bf16>{{}, (bf16*)out, (bf16*)out_gate, (bf16*)out_up, activation, whole}, dtype, ws, st);
+    else
+        gated_forward(g, Gate<float>{{}, (float*)out, (float*)out_gate, (float*)out_up, activation, whole}, dtype, ws, st);
+    return launched();
+}
+
+extern "C" size_t spec_gated_linear_grad_workspace_bytes(spec_dtype dtype, int M, int N, int K) {
+    return gated_ok(dtype, M, N, K) ? gated_layout(dtype, M, N, K).total : 0;
+}
+
+extern "C" spec_status spec_gated_linear_grad(const void* x, const void* gate, const void* up, const void* gate_preact,
+                                              const void* up_preact, const void* grad_out, spec_dtype dtype,
+                                              spec_activation activation, int M, int N, int K, void* grad_x, void* grad_gate,
+                                              void* grad_up, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!type_ok(dtype)) return SPEC_EDTYPE;
+    if (!gated_ok(dtype, M, N, K) || !act_ok(activation) || !gate_preact || !up_preact || !grad_out) return SPEC_EINVAL;
+    if ((grad_x && (!gate || !up)) || ((grad_gate || grad_up) && !x)) return SPEC_EINVAL;
+    if (!ws_ok(workspace, workspace_bytes, spec_gated_linear_grad_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    if (value_of(dtype) == SPEC_BF16)
+        gated_backward<bf16>(x, gate, up, gate_preact, up_preact, grad_out, activation, M, N, K, grad_x, grad_gate, grad_up, dtype, ws, st);
+    else
+        gated_backward<float>(x, gate, up, gate_preact, up_preact, grad_out, activation, M, N, K, grad_x, grad_gate, grad_up, dtype, ws, st);
+    return launched();
+}

@@ -1,0 +1,467 @@
+// product.h -- the tiled matrix product under the operators that train a head:
+// out[m][n] = sum_k X[m][k] W[n][k], finished by an epilogue of the operator's
+// own.  Either operand may lie with k along its rows ("by rows": X[m][k]) or
+// down them ("by k": X[k][m]), so that no gradient needs a turned copy.
+#ifndef SPEC_PRODUCT_H
+#define SPEC_PRODUCT_H
+
+#include "tiles.h"
+
+namespace {
+
+struct Product {
+    const void *x[2], *w[2];  // [1]: of a second sum over k, a second product, or a pair's other matrix
+    int64_t ldx, ldw;         // elements from row to row, or from k to k
+    int M, N, K;
+    int K2;                   // length of a second sum that is added to the first, or 0
+    const int *live_m, *live_k;  // on the device: the count that stands for M, or for K, or null
+    int products;             // 1, or 2: x[0] and x[1] with the same w
+    int splits;               // of the sum over k
+};
+
+// One tile's shape.  XK, WK: the operand lies by k.  PAIR: w[0] and w[1] are
+// multiplied side by side, BN / 2 rows of each, every wave with the same rows of
+// both.  DIRECT: 16-byte aligned rows, loaded straight to LDS.  ONCE: W is read
+// once and not to be kept in the caches.
+template <typename T_, int BM_, int BN_, int WM_, int WN_, int STAGES_, bool XK_, bool WK_, bool PAIR_, bool DIRECT_, bool ONCE_ = false>
+struct Tile {
+    using T = T_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+    static constexpr bool XK = XK_, WK = WK_, PAIR = PAIR_, DIRECT = DIRECT_, ONCE = ONCE_;
+    static constexpr int kElems = 16 / (int)sizeof(T), kStep = 8 * kElems;  // k of a stage: 128 bytes of a row
+    static constexpr int FM = WM / 32, FN = WN / 32, kWavesM = BM / WM, kWavesN = BN / WN;
+    static constexpr int kColsN = PAIR ? BN / 2 : BN;  // columns of the result
+    static constexpr int kWaveN = PAIR ? WN / 2 : WN;
+    static constexpr int kStageBytes = (BM + BN) * 128;
+    static_assert(kWavesM * kWavesN == kThreads / 64, "four waves");
+    static_assert(!PAIR || (WN >= 64 && !WK), "whole blocks of each of a pair");
+};
+
+// How an operand of B rows lies in a stage: 128 bytes of k of each row, or k
+// after k of B elements.  A load is 1 KiB, lane after lane 16 bytes.  Chunks
+// are exchanged within their row so that the reads of an instruction's operand
+// use each bank once: by rows, sixteen rows are read at one chunk; by k in
+// bf16, four k of 64 neighbouring bytes at once; in fp32, 128 bytes of two k
+// that are four apart.
+template <typename T, int B, bool K>
+struct Lies {
+    static constexpr int kRowBytes = K ? B * (int)sizeof(T) : 128, kRowChunks = kRowBytes / 16;
+    static constexpr int kRows = 64 / kRowChunks, kLoads = B / 32;
+    static_assert(kRows * kRowChunks == 64, "whole rows a load");
+    __device__ static int row(int i, int w, int lane) { return (i * 4 + w) * kRows + lane / kRowChunks; }
+    __device__ static int swizzle(int r) {
+        if constexpr (!K) return r >> 1 & 7;
+        else if constexpr (sizeof(T) == 2) return kRowBytes >= 256 ? (r & 3) << 2 : kRowBytes == 128 ? (r >> 1 & 1) << 2 : 0;
+        else return kRowBytes >= 256 ? (r >> 2 & 1) << 3 : 0;
+    }
+    __device__ static int chunk(int i, int w, int lane) { return lane % kRowChunks ^ swizzle(row(i, w, lane)); }
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+// The chunk pair's operand of 32 rows from r0 on: lane l has row r0 + l % 32 and
+// chunk 2 pair + l / 32.  A stage that lies by k is read turned: in bf16 by the
+// LDS's own transposing reads, four k of sixteen rows to a group of lanes.
+template <typename T, int B, bool K>
+__device__ inline u32x4 operand(const char* at, int pair, int r0, int lane) {
+    using L = Lies<T, B, K>;
+    const int l = lane & 31, h = lane >> 5;
+    if constexpr (!K) {
+        return *reinterpret_cast<const u32x4*>(at + (r0 + l) * 128 + ((2 * pair + h) ^ L::swizzle(l)) * 16);
+    } else if constexpr (sizeof(T) == 2) {
+        const int k = (lane & 15) >> 2;
+        const char* p = at + ((2 * pair + h) * 8 + k) * L::kRowBytes + (r0 * 2 ^ L::swizzle(k) * 16) + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * L::kRowBytes));
+        const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+        return (u32x4){x[0], x[1], y[0], y[1]};
+    } else {
+        const char* p = at + (2 * pair + h) * 4 * L::kRowBytes + ((r0 + l) * 4 ^ L::swizzle(4 * h) * 16);
+        u32x4 q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint32_t*>(p + i * L::kRowBytes);
+        return q;
+    }
+}
+
+// Where a wave's part of the result lies.
+struct Part {
+    int m0, n0;       // its first row and column
+    int M, N;         // of the whole result
+    int lane, w;      // of the workgroup's waves
+    int tm, tn;       // the workgroup's tile
+    int split, product;
+    char* lds;        // the workgroup's, free to use
+};
+
+// A wave's blocks of the j-th 32 rows of m, laid in its own part of the LDS so
+// that neighbouring lanes may take neighbouring n: row r at rows + r * (WN + 4).
+template <class C>
+__device__ inline float* rows_of(const Part& p) {
+    static_assert(4 * 32 * (C::WN + 4) * 4 <= C::STAGES * C::kStageBytes, "the rows fit");
+    return reinterpret_cast<float*>(p.lds) + p.w * 32 * (C::WN + 4);
+}
+template <class C, class J>
+__device__ __attribute__((always_inline)) inline void lay(const Part& p, f32x16 (&acc)[C::FN][C::FM], J j) {
+    float* rows = rows_of<C>(p) + (p.lane & 31) * (C::WN + 4) + (p.lane >> 5) * 4;
+    each(std::make_integer_sequence<int, C::FN * 4>(), [&](auto u) __attribute__((always_inline)) {
+        constexpr int i = u / 4, q = u % 4;
+        *reinterpret_cast<f32x4*>(rows + i * 32 + q * 8) =
+            (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    });
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+// All of them in turn: f(j, rows).
+template <class C, typename F>
+__device__ __attribute__((always_inline)) inline void turned(const Part& p, f32x16 (&acc)[C::FN][C::FM], F f) {
+    each(std::make_integer_sequence<int, C::FM>(), [&](auto j) __attribute__((always_inline)) {
+        lay<C>(p, acc, j);
+        f(j, rows_of<C>(p));
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    });
+}
+
+// The product.  E::start<C>(part, acc) may set what the sums start from, and
+// E::finish<C>(part, acc) takes each wave's sums: acc[i][j] is a 32 x 32 block,
+// lane l with row l % 32 of m, value 4 q + r with column 8 q + 4 (l / 32) + r of
+// n.
+template <class C, class E>
+__global__ __launch_bounds__(kThreads, C::kStageBytes * C::STAGES <= 80 * 1024 ? 2 : 1) void k_product(Product g, E e) {
+    using T = typename C::T;
+    using LX = Lies<T, C::BM, C::XK>;
+    using LW = Lies<T, C::BN, C::WK>;
+    constexpr int BM = C::BM, BN = C::BN, FM = C::FM, FN = C::FN, STAGES = C::STAGES;
+    constexpr int kElems = C::kElems, kStep = C::kStep, kLoadsW = LW::kLoads, kLoads = kLoadsW + LX::kLoads;
+    constexpr int kStageBytes = C::kStageBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[STAGES][kStageBytes];
+    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int M = g.live_m ? __builtin_amdgcn_readfirstlane(*g.live_m) : g.M;
+    const int K = g.live_k ? __builtin_amdgcn_readfirstlane(*g.live_k) : g.K;
+    const unsigned tiles_m = (M + BM - 1) / BM, tiles_n = (g.N + C::kColsN - 1) / C::kColsN, tiles = tiles_m * tiles_n;
+    if (blockIdx.x >= tiles * (unsigned)(g.splits * g.products)) return;
+    const int turn = blockIdx.x / tiles, split = turn % g.splits, product = turn / g.splits;
+    int tm, tn;
+    tile_of(blockIdx.x % tiles, tiles, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * C::kColsN;
+    const int wm = w / C::kWavesN * C::WM, wn = w % C::kWavesN * C::WN;
+
+    // The order of the sum's steps: the whole ones of both sums, then what is
+    // left of each.  This split's are [begin, end).
+    const int whole1 = K / kStep, whole = whole1 + g.K2 / kStep;
+    const int rest1 = K % kStep != 0, steps = whole + rest1 + (g.K2 % kStep != 0);
+    const int per = (steps + g.splits - 1) / g.splits, begin = split * per, end = min(steps, begin + per);
+    auto second = [&](int s) { return s < whole ? s >= whole1 : s >= whole + rest1; };
+    auto k_of = [&](int s) {
+        if (s < whole) return (s < whole1 ? s : s - whole1) * kStep;
+        return (second(s) ? g.K2 : K) / kStep * kStep;
+    };
+    // row r of W's part of a stage: which matrix of a pair, and its column n
+    auto pair_of = [](int r) { return C::PAIR && r % C::WN >= C::kWaveN; };
+    auto col_of = [](int r) { return C::PAIR ? r / C::WN * C::kWaveN + r % C::kWaveN : r; };
+    auto x_at = [&](int s) {
+        const int i = g.products == 2 ? product : second(s);
+        return static_cast<const T*>(g.x[i]) + (C::XK ? (int64_t)k_of(s) * g.ldx + m0 : m0 * g.ldx + k_of(s));
+    };
+    auto w_at = [&](int s, bool other) {
+        const int i = C::PAIR ? other : second(s);
+        return static_cast<const T*>(g.w[i]) + (C::WK ? (int64_t)k_of(s) * g.ldw + n0 : n0 * g.ldw + k_of(s));
+    };
+
+    // offsets of this lane's loads; what lies past the matrix reads a row or
+    // column that does not: those sums are dropped
+    uint32_t off[C::DIRECT ? kLoads : 1];
+    if constexpr (C::DIRECT)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            int64_t at;
+            if (i < kLoadsW) {
+                const int r = LW::row(i, w, lane), c = LW::chunk(i, w, lane);
+                at = C::WK ? r * g.ldw + (c * kElems < g.N - n0 ? c * kElems : 0) : min(col_of(r), g.N - 1 - n0) * g.ldw + c * kElems;
+            } else {
+                const int r = LX::row(i - kLoadsW, w, lane), c = LX::chunk(i - kLoadsW, w, lane);
+                at = C::XK ? r * g.ldx + (c * kElems < M - m0 ? c * kElems : 0) : min(r, M - 1 - m0) * g.ldx + c * kElems;
+            }
+            off[i] = (uint32_t)(at * (int64_t)sizeof(T));
+        }
+    // loads [FROM, TO) of a whole step into a stage
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&lds[0][0] + w * 1024;
+    auto rsrc_of = [](const T* p) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), (short)0, 0x7fffffff, 0x00020000); };
+    auto load_direct = [&](int stage, int s, auto from, auto to) {
+        if constexpr (C::DIRECT) {
+            const uint32_t base = lds0 + stage * kStageBytes;
+            const __amdgpu_buffer_rsrc_t rx = rsrc_of(x_at(s)), rw = rsrc_of(w_at(s, false)), rp = rsrc_of(w_at(s, C::PAIR));
+            each(std::make_integer_sequence<int, kLoads>(), [&](auto i) {
+                if constexpr (i >= from && i < to) {
+                    if constexpr (i >= kLoadsW)
+                        to_lds<i * 4096, false>(rx, base, off[i], 0);
+                    else if constexpr (C::PAIR && i * 32 % C::WN >= C::kWaveN)
+                        to_lds<i * 4096, C::ONCE>(rp, base, off[i], 0);
+                    else
+                        to_lds<i * 4096, C::ONCE>(rw, base, off[i], 0);
+                }
+            });
+        }
+    };
+    using Zero = std::integral_constant<int, 0>;
+    using All = std::integral_constant<int, kLoads>;
+    // any step through registers, at any alignment, zero past the sum's end
+    auto fetch = [&](int s, u32x4 (&q)[kLoads]) {
+        const int left = (second(s) ? g.K2 : K) - k_of(s);
+        const T *px = x_at(s), *pw[2] = {w_at(s, false), w_at(s, C::PAIR)};
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const bool x = i >= kLoadsW;
+            const int r = x ? LX::row(i - kLoadsW, w, lane) : LW::row(i, w, lane);
+            const int c = (x ? LX::chunk(i - kLoadsW, w, lane) : LW::chunk(i, w, lane)) * kElems;
+            const int64_t ld = x ? g.ldx : g.ldw;
+            const int rows = x ? M - m0 : g.N - n0;
+            if (x ? C::XK : C::WK) {
+                q[i] = (u32x4){0, 0, 0, 0};
+                if (r < left) q[i] = chunk_of((x ? px : pw[0]) + r * ld, c, rows);
+            } else {
+                const T* p = x ? px + min(r, rows - 1) * ld : pw[pair_of(r)] + min(col_of(r), rows - 1) * ld;
+                q[i] = chunk_of(p, c, left);
+            }
+        }
+    };
+    auto place = [&](int stage, const u32x4 (&q)[kLoads]) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) *reinterpret_cast<u32x4*>(&lds[stage][(i * 4 + w) * 1024 + lane * 16]) = q[i];
+    };
+
+    const Part part{m0 + wm, n0 + w % C::kWavesN * C::kWaveN, M, g.N, lane, w, tm, tn, split, product, &lds[0][0]};
+    f32x16 acc[FN][FM] = {};
+    e.template start<C>(part, acc);
+    // Operands of one pair of chunks, read from LDS a pair ahead of their use.
+    constexpr int kPairs = 4, kProducts = FN * FM, kReads = FN + FM;
+    struct Operands {
+        u32x4 a[FN], b[FM];
+    };
+    Operands f[2];
+    auto read = [&](int stage, int pair, int i, Operands& o) {
+        const char* at = &lds[0][0] + stage * kStageBytes;
+        if (i < FM)
+            o.b[i] = operand<T, BM, C::XK>(at + BN * 128, pair, wm + i * 32, lane);
+        else
+            o.a[i - FM] = operand<T, BN, C::WK>(at, pair, wn + (i - FM) * 32, lane);
+    };
+    // The products of one pair, with `between` called for each before it: the
+    // order is kept, so that reads and loads sit under the products.
+    auto multiply = [&](const Operands& o, auto&& between) {
+        each(std::make_integer_sequence<int, kProducts>(), [&](auto i) {
+            between(i);
+            acc[i / FM][i % FM] = mfma32(T(), o.a[i / FM], o.b[i % FM], acc[i / FM][i % FM]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // the next pair's operands are read under the first products
+    auto read_under = [&](auto i, int stage, int pair, Operands& o) {
+        constexpr int from = kProducts > kReads ? (i < kReads ? i : kReads) : i * kReads / kProducts;
+        constexpr int to = kProducts > kReads ? (i + 1 < kReads ? i + 1 : kReads) : (i + 1) * kReads / kProducts;
+#pragma unroll
+        for (int r = from; r < to; ++r) read(stage, pair, r, o);
+    };
+
+    int s = begin;
+    if constexpr (C::DIRECT) {
+        const int stop = min(end, whole), full = max(0, stop - begin);
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i)
+            if (i < full) load_direct(i, begin + i, Zero(), All());
+        if (full >= STAGES)
+            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(kLoads * (STAGES - 1)) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        int slot = 0;
+        // All but the last pair of a stage.  LOADS: with the second half of the
+        // loads of `step` into the stage that was freed last.
+        auto inner = [&](auto loads, int freed, int step) {
+            each(std::make_integer_sequence<int, kPairs - 1>(), [&](auto p) {
+                multiply(f[p & 1], [&](auto i) {
+                    read_under(i, slot, p + 1, f[(p + 1) & 1]);
+                    if constexpr (loads && p == 0) {
+                        constexpr int h = kLoads / 2, m = kLoads - h;
+                        load_direct(freed, step, std::integral_constant<int, h + i * m / kProducts>(),
+                                    std::integral_constant<int, h + (i + 1) * m / kProducts>());
+                    }
+                });
+            });
+        };
+        // A stage's last pair and the next stage's others.  Before it the next
+        // stage's loads have arrived, in every wave, and every wave has this
+        // stage's last operands, so that it can be filled anew: half of the
+        // loads under this pair, half under the next.
+        auto advance = [&](auto loads, int step) {
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            const int freed = slot;
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            multiply(f[1], [&](auto i) {
+                read_under(i, slot, 0, f[0]);
+                if constexpr (loads) {
+                    constexpr int h = kLoads / 2;
+                    load_direct(freed, step, std::integral_constant<int, i * h / kProducts>(),
+                                std::integral_constant<int, (i + 1) * h / kProducts>());
+                }
+            });
+            inner(loads, freed, step);
+        };
+        if (full > 0) {
+#pragma unroll
+            for (int i = 0; i < kReads; ++i) read(0, 0, i, f[0]);
+            inner(std::false_type(), 0, 0);
+            int n = STAGES;
+            for (; n < full; ++n) {
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"(kLoads * (STAGES - 2)) : "memory");
+                advance(std::true_type(), begin + n);
+            }
+            for (n = n - STAGES + 1; n < full; ++n) {
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                advance(std::false_type(), 0);
+            }
+            multiply(f[1], [](auto) {});
+            s = stop;
+        }
+    }
+    // what is no whole step, or not aligned: the next step's loads are on
+    // their way while one is worked on
+    if (s < end) {
+        u32x4 q[kLoads];
+        fetch(s, q);
+        for (; s < end; ++s) {
+            __syncthreads();
+            place(0, q);
+            __syncthreads();
+            if (s + 1 < end) fetch(s + 1, q);
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+#pragma unroll
+                for (int i = 0; i < kReads; ++i) read(0, p, i, f[0]);
+                multiply(f[0], [](auto) {});
+            }
+        }
+    }
+    __syncthreads();
+    e.template finish<C>(part, acc);
+}
+
+// ------------------------------------------------------------- plain epilogue
+struct FromZero {
+    template <class C>
+    __device__ void start(const Part&, f32x16 (&)[C::FN][C::FM]) const {}
+};
+// The sums as they are: rounded to O, or added to (ADD) or set as fp32 parts
+// [split][M][ld].
+template <typename O>
+struct Store : FromZero {
+    O* out[2];       // of each product
+    int64_t ld;      // from row to row
+    int64_t splits;  // from split to split
+    bool add, whole;  // whole: four at once
+    template <class C>
+    __device__ __attribute__((always_inline)) void finish(const Part& p, f32x16 (&acc)[C::FN][C::FM]) const {
+        static_assert(!C::PAIR, "one matrix");
+        constexpr int kLanes = C::WN / 4, kAtOnce = 64 / kLanes, kPitch = C::WN + 4;
+        const int c = p.lane % kLanes * 4, n = p.n0 + c;
+        O* to0 = out[p.product] + p.split * splits + n;
+        turned<C>(p, acc, [&](int j, float* rows) __attribute__((always_inline)) {
+            if (n >= p.N) return;
+#pragma unroll 4
+            for (int r = p.lane / kLanes; r < 32; r += kAtOnce) {
+                const int m = p.m0 + j * 32 + r;
+                if (m >= p.M) break;
+                const f32x4 q = *reinterpret_cast<const f32x4*>(rows + r * kPitch + c);
+                float v[4] = {q[0], q[1], q[2], q[3]};
+                O* to = to0 + m * ld;
+                if (whole) {
+                    if (add) {
+                        float o[4];
+                        get4(to, o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] += o[i];
+                    }
+                    put4(to, v);
+                } else {
+                    for (int i = 0; i < 4 && n + i < p.N; ++i) put(to + i, add ? to_f(to[i]) + v[i] : v[i]);
+                }
+            }
+        });
+    }
+};
+inline bool fours(const void* p, int64_t ld, size_t elem_bytes) { return ld % 4 == 0 && (uintptr_t)p % (4 * elem_bytes) == 0; }
+
+// Adds the splits' sums [splits][rows][N] in their order and rounds them.  row:
+// where each row of the result stands among the summed ones, -1 for a row of
+// zeros; null: in place.  Four columns a thread.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_join(const float* part, int splits, int64_t stride, const int* row, int M, int N, T* out) {
+    const int across = (N + 3) / 4;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int m = (int)(i / across), n = (int)(i % across) * 4;
+    if (m >= M) return;
+    const int from = row ? row[m] : m;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (from >= 0)
+        for (int s = 0; s < splits; ++s) {
+            const float* p = part + s * stride + (int64_t)from * N + n;
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) v[j] += p[j];
+        }
+    for (int j = 0; j < 4; ++j)
+        if (n + j < N) put(out + (int64_t)m * N + n + j, v[j]);
+}
+
+// ---------------------------------------------------------------- host side
+inline unsigned four_blocks(long long M, long long N) { return (unsigned)((M * ((N + 3) / 4) + kThreads - 1) / kThreads); }
+
+// The tile: the largest that still gives kEnough workgroups and does not compute
+// more than a quarter more past the edges.  Where tiles of 64 leave compute
+// units idle, the sum over k is split.
+constexpr int kEnough = 200, kSplitGroups = 512, kMaxSplits = 16;
+enum Size { kTile256, kTile128, kTile64 };
+inline long long tiles_at(long long M, long long N, int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); }
+inline Size size_of(long long M, long long N, int products) {
+    auto fits = [&](int b) {
+        return tiles_at(M, N, b) * products >= kEnough && tiles_at(M, N, b) * 16 <= tiles_at(M, N, b / 2) * 5;
+    };
+    return fits(256) ? kTile256 : fits(128) ? kTile128 : kTile64;
+}
+inline long long step_of(spec_dtype d) { return 128 / (long long)elem(d); }
+inline int splits_at(spec_dtype d, long long M, long long N, long long K, int products) {
+    if (size_of(M, N, products) != kTile64) return 1;
+    const long long steps = (K + step_of(d) - 1) / step_of(d), want = kSplitGroups / (tiles_at(M, N, 64) * products);
+    long long s = want < steps / 4 ? want : steps / 4;
+    s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+    const long long per = (steps + s - 1) / s;
+    return (int)((steps + per - 1) / per);  // no split without steps
+}
+
+template <class C, class E>
+void launch_tile(const Product& g, const E& e, hipStream_t st) {
+    const unsigned grid = (unsigned)((g.M + C::BM - 1) / C::BM) * (unsigned)((g.N + C::kColsN - 1) / C::kColsN) *
+                          (unsigned)(g.splits * g.products);
+    k_product<C, E><<<grid, kThreads, 0, st>>>(g, e);
+}
+inline bool aligned(const Product& g, size_t e) {
+    uintptr_t a = (uintptr_t)g.x[0] | (uintptr_t)g.w[0] | (uintptr_t)g.x[1] | (uintptr_t)g.w[1];
+    return a % 16 == 0 && g.ldx * e % 16 == 0 && g.ldw * e % 16 == 0;
+}
+// g.splits stands for a tile of 64, like `size`, whatever the alignment.
+template <typename T, bool XK, bool WK, class E>
+void launch_product(const Product& g, const E& e, Size size, hipStream_t st) {
+    if (!aligned(g, sizeof(T)))
+        launch_tile<Tile<T, 64, 64, 32, 32, 2, XK, WK, false, false>>(g, e, st);
+    else if (size == kTile256)
+        launch_tile<Tile<T, 256, 256, 128, 128, 2, XK, WK, false, true>>(g, e, st);
+    else if (size == kTile128)
+        launch_tile<Tile<T, 128, 128, 64, 64, 4, XK, WK, false, true>>(g, e, st);
+    else
+        launch_tile<Tile<T, 64, 64, 32, 32, 4, XK, WK, false, true>>(g, e, st);
+}
+
+}  // namespace
+
+#endif  // SPEC_PRODUCT_H

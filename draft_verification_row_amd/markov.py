@@ -22,24 +22,44 @@ costs `draft_cost` target passes: tokens / (passes * (1 + K * draft_cost)).
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
-from . import (SpecVerifyError, _check, spec_linear, spec_sample_drafts,
-               spec_sample_workspace_bytes, spec_verify_exact, spec_verify_workspace_bytes)
+from . import (SpecVerifyError, _check, spec_cross_entropy, spec_embedding, spec_gated_linear,
+               spec_linear, spec_sample_drafts, spec_sample_workspace_bytes, spec_verify_exact,
+               spec_verify_workspace_bytes)
 
-__all__ = ["HeadModel", "SpeculativeTrace", "SpeculativeGraph", "generate_speculative",
-           "head_logits", "trace_stats"]
+__all__ = ["GatedBlock", "HeadModel", "SpeculativeTrace", "SpeculativeGraph",
+           "generate_speculative", "head_logits", "head_loss", "trace_stats"]
+
+
+class GatedBlock(NamedTuple):
+    """A block h + (silu(h gate^T) * (h up^T)) down^T."""
+    gate: torch.Tensor  # [F][H]
+    up: torch.Tensor    # [F][H]
+    down: torch.Tensor  # [H][F]
 
 
 class HeadModel(NamedTuple):
     """A next-token model made of a draft head's parts, one dtype throughout:
-    the last token's embedding h, residual blocks h + silu(h W^T + b), and the
-    output layer.  It may stand wherever a logit table may."""
-    embedding: torch.Tensor                                # [V][H]
-    blocks: Sequence[Tuple[torch.Tensor, torch.Tensor]]    # (W [H][H], b [H]) each
-    output: torch.Tensor                                   # [V][H]
+    the last token's embedding h, residual blocks h + silu(h W^T + b) or
+    GatedBlocks, and the output layer.  It may stand wherever a logit table
+    may."""
+    embedding: torch.Tensor       # [V][H]
+    blocks: Sequence[Union[Tuple[torch.Tensor, torch.Tensor], GatedBlock]]  # (W [H][H], b [H])
+    output: torch.Tensor          # [V][H]
+
+
+def _through(blocks, h):
+    """h after the blocks."""
+    for block in blocks:
+        if isinstance(block, GatedBlock):
+            h = spec_linear(spec_gated_linear(h, block.gate, block.up), block.down, residual=h)
+        else:
+            weight, bias = block
+            h = spec_linear(h, weight, bias, residual=h, activation="silu")
+    return h
 
 
 def head_logits(model: HeadModel, tokens: torch.Tensor, *,
@@ -48,9 +68,16 @@ def head_logits(model: HeadModel, tokens: torch.Tensor, *,
     on the GPU): [*tokens.shape][V] in out_dtype (the model's by default).  The
     parameters have gradients."""
     h = model.embedding[tokens].contiguous()  # a view of tokens gives a view
-    for weight, bias in model.blocks:
-        h = spec_linear(h, weight, bias, residual=h, activation="silu")
-    return spec_linear(h, model.output, out_dtype=out_dtype)
+    return spec_linear(_through(model.blocks, h), model.output, out_dtype=out_dtype)
+
+
+def head_loss(model: HeadModel, tokens: torch.Tensor, targets: torch.Tensor) -> torch.Tensor:
+    """The model's cross entropy, float32 [*tokens.shape]: -log p(target) after
+    each token, with no logits in memory.  tokens and targets int32, -1 for a
+    padded position (a padded token's embedding is zero, a padded target's loss
+    0).  The parameters have gradients."""
+    h = _through(model.blocks, spec_embedding(model.embedding, tokens))
+    return spec_cross_entropy(h, model.output, targets).loss
 
 
 class SpeculativeTrace(NamedTuple):
@@ -71,9 +98,18 @@ def _model(model, name):
         raise SpecVerifyError(f"{name}.embedding must be [V][H]")
     V, H = E.shape
     _check(model.output, f"{name}.output", E.dtype, (V, H))
-    for i, (weight, bias) in enumerate(model.blocks):
-        _check(weight, f"{name}.blocks[{i}] weight", E.dtype, (H, H))
-        _check(bias, f"{name}.blocks[{i}] bias", E.dtype, (H,))
+    for i, block in enumerate(model.blocks):
+        at = f"{name}.blocks[{i}]"
+        if isinstance(block, GatedBlock):
+            gate = _check(block.gate, f"{at} gate", E.dtype)
+            if gate.dim() != 2 or gate.shape[1] != H:
+                raise SpecVerifyError(f"{at} gate must be [F][{H}]")
+            _check(block.up, f"{at} up", E.dtype, gate.shape)
+            _check(block.down, f"{at} down", E.dtype, (H, gate.shape[0]))
+            continue
+        weight, bias = block
+        _check(weight, f"{at} weight", E.dtype, (H, H))
+        _check(bias, f"{at} bias", E.dtype, (H,))
     return V, None if E.dtype == torch.bfloat16 else E.dtype
 
 
@@ -101,7 +137,8 @@ def _models(target, draft) -> _Models:
 def _held(model):
     """The model with its blocks in tuples, which no one else can change."""
     if isinstance(model, HeadModel):
-        return model._replace(blocks=tuple((weight, bias) for weight, bias in model.blocks))
+        return model._replace(blocks=tuple(b if isinstance(b, GatedBlock) else (b[0], b[1])
+                                           for b in model.blocks))
     return model
 
 

@@ -603,6 +603,98 @@ spec_status spec_linear_grad(const void *x, const void *weight, const void *prea
                              void *grad_weight, void *grad_bias, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/*
+ * The rows of an embedding table that tokens pick, scaled: out[i] = scale *
+ * W[tokens[i]], the product rounded once.  A token of -1 (padding) gives a row
+ * of zeros, any other outside [0, V) a row of NaN.
+ *
+ *   weight (W) [V][H], out [n][H] dtype; tokens [n] int32
+ * 1 <= n, V, H <= SPEC_MAX_LINEAR, and n * H and V * H below 2^34.
+ */
+spec_status spec_embedding(const void *weight, spec_dtype dtype, const int32_t *tokens,
+                           float scale, int n, int V, int H, void *out, void *stream);
+
+/* Its gradient, the whole table's: grad_weight[v] = scale * the sum of
+ * grad_out[i] over the i with tokens[i] = v, in fp32 in a fixed order, rounded
+ * once; zeros for a token that does not occur.  Rows of grad_out of tokens
+ * outside the table are not read.  The workspace needs no initialization and
+ * is left with any contents. */
+size_t spec_embedding_grad_workspace_bytes(spec_dtype dtype, int n, int V, int H);
+spec_status spec_embedding_grad(const int32_t *tokens, const void *grad_out, spec_dtype dtype,
+                                float scale, int n, int V, int H, void *grad_weight,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The gated block that a draft head may have in a residual block's place:
+ * y = act(x G^T) * (x U^T), element by element, both products in one kernel.
+ * They are summed in fp32, y is formed from the sums and rounded once.
+ *
+ *   x [M][K], gate (G), up (U) [N][K], out [M][N]     dtype
+ *   out_gate, out_up [M][N] dtype, or both NULL: x G^T and x U^T, which the
+ *                gradients need
+ * Any activation of spec_linear.  1 <= M, N, K <= SPEC_MAX_LINEAR, and M * N,
+ * M * K and N * K below 2^33.  The workspaces need no initialization and are
+ * left with any contents, as spec_linear's.
+ */
+size_t spec_gated_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K);
+spec_status spec_gated_linear(const void *x, const void *gate, const void *up, spec_dtype dtype,
+                              spec_activation activation, int M, int N, int K, void *out,
+                              void *out_gate, void *out_up, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Its gradients: with dg = grad_out up_preact act'(gate_preact) and du =
+ * grad_out act(gate_preact), both rounded to dtype, grad_x = dg G + du U,
+ * grad_gate = dg^T x and grad_up = du^T x.  A NULL output is not computed;
+ * gate and up are read for grad_x, x for the others.  Everything in dtype. */
+size_t spec_gated_linear_grad_workspace_bytes(spec_dtype dtype, int M, int N, int K);
+spec_status spec_gated_linear_grad(const void *x, const void *gate, const void *up,
+                                   const void *gate_preact, const void *up_preact,
+                                   const void *grad_out, spec_dtype dtype,
+                                   spec_activation activation, int M, int N, int K, void *grad_x,
+                                   void *grad_gate, void *grad_up, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/*
+ * The cross entropy of given tokens under a head's output layer, without its
+ * logits z = x W^T + bias in memory: out_loss[m] = -log softmax(z_m)[tokens[m]]
+ * and out_lse[m] = log sum e^(z_m), in nats, from fp32 products and sums.
+ * tokens[m] = -1 marks a padded row, which does not enter any result: its loss
+ * and lse are 0, and its row of x is not used.  A bias of -inf takes a token
+ * out of the vocabulary: its probability is 0, a row with that token has a
+ * loss of +inf, and a row with nothing left has a loss of +inf and an lse of
+ * -inf.  A row with a NaN or +inf among its logits gives NaN.
+ *
+ *   x [M][K], weight (W) [V][K], bias [V] or NULL    dtype
+ *   tokens [M] int32; out_loss, out_lse [M] float
+ *   out_status [M] int32: 0, or 1 for a token outside [-1, V): the row is then
+ *              treated as padded
+ *   out_stats [M][2] float or NULL: what the gradient needs
+ * 1 <= M, V, K <= SPEC_MAX_LINEAR, and M * K and V * K below 2^33.  The
+ * workspaces need no initialization and are left with any contents, as
+ * spec_linear's.
+ */
+size_t spec_cross_entropy_workspace_bytes(spec_dtype dtype, int M, int V, int K);
+spec_status spec_cross_entropy(const void *x, const void *weight, const void *bias,
+                               spec_dtype dtype, const int32_t *tokens, int M, int V, int K,
+                               float *out_loss, float *out_lse, int32_t *out_status,
+                               float *out_stats, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* The gradient of sum_m grad_loss[m] loss[m] + grad_lse[m] lse[m] to x, W and
+ * bias, in dtype; either weight may be NULL (zero), and an output that is NULL
+ * is not computed.  With dz = (grad_loss + grad_lse) softmax(z) - grad_loss at
+ * the token, rounded to dtype, grad_x = dz W, grad_weight = dz^T x, and
+ * grad_bias sums dz before its rounding.  Padded rows and rows with no token
+ * left give zeros.  Up to 512 MiB of dz are in the workspace at a time (more
+ * where 1024 tokens of the vocabulary are more).  x, weight, bias, tokens and
+ * stats are the forward call's. */
+size_t spec_cross_entropy_grad_workspace_bytes(spec_dtype dtype, int M, int V, int K);
+spec_status spec_cross_entropy_grad(const void *x, const void *weight, const void *bias,
+                                    spec_dtype dtype, const int32_t *tokens, const float *stats,
+                                    const float *grad_loss, const float *grad_lse, int M, int V,
+                                    int K, void *grad_x, void *grad_weight, void *grad_bias,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,217 @@
+"""spec_gated_linear against its definition in float64, forward and gradients.
+
+Tolerances.  u = 2^-24, h half a step of a type.  A product summed in float32 in
+any order is off by at most (K + 8) 2u sum |x| |w| (2u a step: the matrix
+instructions need not round to nearest).  The activations have slopes of at most
+1.13 and are evaluated to a few u of |g| + 1.  For the gradients, g and u are
+kept in the inputs' type and both slopes rounded to it; |act''| <= 0.8.
+"""
+import math
+
+import pytest
+import torch
+
+import draft_verification_row_amd as sv
+from test_gpu_embedding import DT, U, at_offset, close, half
+
+pytestmark = pytest.mark.gpu
+ACTS = ["none", "relu", "gelu", "silu"]
+
+
+def act(z, name):
+    return {"none": lambda: z, "relu": lambda: z.clamp_min(0), "silu": lambda: z * torch.sigmoid(z),
+            "gelu": lambda: z * 0.5 * torch.erfc(-z / math.sqrt(2))}[name]()
+
+
+def slope(z, name):
+    if name == "relu":
+        return (z > 0).double()
+    if name == "silu":
+        s = torch.sigmoid(z)
+        return s * (1 + z * (1 - s))
+    if name == "gelu":
+        return 0.5 * torch.erfc(-z / math.sqrt(2)) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    return torch.ones_like(z)
+
+
+def make(M, N, K, dt, seed, off=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    t = [r(M, K).to(dt), (r(N, K) / math.sqrt(K)).to(dt), (r(N, K) / math.sqrt(K)).to(dt)]
+    return [at_offset(v, off) for v in t], at_offset(r(M, N).to(dt), off)
+
+
+def check(M, N, K, dtype="bf16", activation="silu", backward=True, seed=0, off=0):
+    dt = DT[dtype]
+    h = half(dt)
+    live, gy = make(M, N, K, dt, seed + M + N + K, off)
+    live = [v.requires_grad_(backward) for v in live]
+    y = sv.spec_gated_linear(*live, activation=activation)
+    assert y.dtype == dt and y.shape == (M, N)
+    x, wg, wu = (v.detach().double() for v in live)
+    g, u = x @ wg.t(), x @ wu.t()
+    eg, eu = (2 * U * (K + 9) * (x.abs() @ w.abs().t()) for w in (wg, wu))
+    f = act(g, activation)
+    ef = 1.13 * eg + 8 * U * (g.abs() + 1)
+    want = f * u
+    ey = ef * u.abs() + (f.abs() + ef) * eu + 2 * U * want.abs()
+    close(y, want, ey + h * (want.abs() + ey), "y")
+    if not backward:
+        return
+    got = torch.autograd.grad([y], live, [gy])
+    dy = gy.double()
+    s = slope(g, activation)
+    dg, du = dy * u * s, dy * f
+    kg, ku = 1.01 * (eg + h * g.abs()), 1.01 * (eu + h * u.abs())  # the kept ones' errors
+    if activation == "relu":
+        es = (g.abs() <= eg).double()  # may fall on either side of 0
+    else:
+        es = 0.8 * kg + 8 * U * (1 + g.abs())
+    edg = dy.abs() * (s.abs() * ku + (u.abs() + ku) * es) + 2 * U * dg.abs()
+    edg = edg + h * (dg.abs() + edg)
+    edu = dy.abs() * (1.13 * kg + 8 * U * (g.abs() + 1)) + U * du.abs()
+    edu = edu + h * (du.abs() + edu)
+    fg, fu = dg.abs() + edg, du.abs() + edu
+
+    def one(i, val, err, name):
+        close(got[i], val, err + h * (val.abs() + err) + 1e-37, name)
+
+    one(0, dg @ wg + du @ wu, edg @ wg.abs() + edu @ wu.abs() + 2 * U * (2 * N + 8) * (fg @ wg.abs() + fu @ wu.abs()), "grad x")
+    for i, d, e, full, name in ((1, dg, edg, fg, "grad gate"), (2, du, edu, fu, "grad up")):
+        one(i, d.t() @ x, e.t() @ x.abs() + 2 * U * (M + 8) * (full.t() @ x.abs()), name)
+
+
+SIZES = [(1, 1, 1), (1, 7, 3), (2, 64, 64), (3, 100, 31), (1, 4096, 512), (5, 1000, 513), (16, 256, 128), (17, 129, 257),
+         (33, 640, 72), (64, 512, 1024), (65, 130, 130), (100, 1001, 777), (127, 255, 127), (128, 128, 128), (129, 257, 264),
+         (256, 256, 64), (300, 700, 520), (513, 384, 192), (1025, 300, 8)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_gated_sizes(M, N, K, dtype):
+    check(M, N, K, dtype, ACTS[(M + N) % 4])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("activation", ACTS)
+@pytest.mark.parametrize("M,N,K", [(4, 96, 160), (140, 264, 136)])
+def test_gated_activations(M, N, K, activation, dtype):
+    check(M, N, K, dtype, activation)
+
+
+@pytest.mark.parametrize("dtype,off", [("bf16", 1), ("bf16", 4), ("f32", 1)])
+@pytest.mark.parametrize("M,N,K", [(2, 72, 64), (40, 130, 96), (270, 264, 128)])
+def test_gated_alignment(M, N, K, dtype, off):
+    check(M, N, K, dtype, off=off)
+
+
+# every tile of each product, whole and ragged, and rows that are padded first
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(1, 32000, 256), (700, 4096, 2048), (2048, 2304, 1024), (2050, 3333, 4104), (4096, 512, 512),
+                                   (1500, 2000, 777), (1300, 3000, 131), (600, 160, 4096)])
+def test_gated_larger(M, N, K, dtype):
+    check(M, N, K, dtype)
+
+
+def test_gated_long_sums():
+    check(70, 90, 50001, "f32", backward=False)
+    check(100000, 24, 16, "bf16", "gelu")
+    check(3, 40000, 24, "bf16", "none")
+
+
+def test_gated_special_values():
+    """NaN and infinities stay in their rows."""
+    for M in (5, 40):
+        x, wg, wu = (v.bfloat16() for v in (torch.randn(M, 64, device="cuda"), torch.randn(70, 64, device="cuda"), torch.randn(70, 64, device="cuda")))
+        clean = sv.spec_gated_linear(x, wg, wu)
+        x[2, 5] = math.nan
+        y = sv.spec_gated_linear(x, wg, wu)
+        keep = [i for i in range(M) if i != 2]
+        assert y[2].isnan().all() and torch.equal(y[keep], clean[keep])
+    big = torch.tensor([[-300.0], [-20.0], [0.0], [20.0], [300.0]], device="cuda")
+    one = torch.ones(1, 1, device="cuda")
+    for name in ("silu", "gelu"):
+        b = big.clone().requires_grad_()
+        v = sv.spec_gated_linear(b, one, one, activation=name)
+        g, = torch.autograd.grad([v.sum()], [b])
+        f, s = act(big.double(), name), slope(big.double(), name)
+        assert (v.double() - f * big).abs().max() < 1e-2  # 300 * 300 to float32's steps
+        assert (g.double() - (f + s * big)).abs().max() < 1e-4
+
+
+def test_gated_shapes_and_single_gradients():
+    x = torch.randn(2, 3, 40, device="cuda")
+    wg, wu = torch.randn(20, 40, device="cuda"), torch.randn(20, 40, device="cuda")
+    full = [t.clone().requires_grad_() for t in (x, wg, wu)]
+    y = sv.spec_gated_linear(*full)
+    assert y.shape == (2, 3, 20)
+    want = torch.autograd.grad([y.sum()], full)  # an expanded gradient
+    for i in range(3):
+        one = [t.clone().requires_grad_(j == i) for j, t in enumerate((x, wg, wu))]
+        got, = torch.autograd.grad([sv.spec_gated_linear(*one).sum()], [one[i]])
+        assert torch.equal(got, want[i]), i
+    assert sv.spec_gated_linear(x[0, 0], wg, wu).shape == (20,)
+    assert torch.equal(sv.spec_gated_linear(x, wg, wu), y)
+
+
+def test_gated_no_rows():
+    x = torch.empty(0, 40, device="cuda", requires_grad=True)
+    wg, wu = (torch.randn(20, 40, device="cuda", requires_grad=True) for _ in range(2))
+    y = sv.spec_gated_linear(x, wg, wu)
+    assert y.shape == (0, 20)
+    y.sum().backward()
+    assert x.grad.shape == (0, 40) and (wg.grad == 0).all() and (wu.grad == 0).all()
+
+
+def test_gated_gradient_against_differences():
+    """Directional derivatives by central differences of the float64 definition."""
+    M, N, K, h = 6, 50, 70, 1e-4
+    live, gy = make(M, N, K, torch.float32, 5)
+    live = [v.requires_grad_() for v in live]
+    grads = torch.autograd.grad([sv.spec_gated_linear(*live)], live, [gy])
+    dirs = [torch.randn(v.shape, device="cuda").double() for v in live]
+
+    def f(s):
+        x, a, b = (v.detach().double() + s * d for v, d in zip(live, dirs))
+        return (act(x @ a.t(), "silu") * (x @ b.t()) * gy.double()).sum()
+
+    want = float((f(h) - f(-h)) / (2 * h))
+    got = float(sum((g.double() * d).sum() for g, d in zip(grads, dirs)))
+    assert abs(got - want) < 1e-2 + 1e-5 * abs(want)
+
+
+def test_gated_writes_nothing_behind_its_outputs():
+    lib = sv.load_library()
+    st = torch.cuda.current_stream().cuda_stream
+    for M, N, K in ((3, 70, 64), (130, 129, 72), (300, 264, 129)):
+        (x, a, b), gy = make(M, N, K, torch.bfloat16, 1)
+        sizes = dict(y=M * N, g=M * N, u=M * N, gx=M * K, gg=N * K, gu=N * K)
+        o = {k: torch.full((n + 512,), 7.0, dtype=torch.bfloat16, device="cuda") for k, n in sizes.items()}
+        p = {k: t.data_ptr() for k, t in o.items()}
+        n1, n2 = lib.spec_gated_linear_workspace_bytes(1, M, N, K), lib.spec_gated_linear_grad_workspace_bytes(1, M, N, K)
+        w1, w2 = (torch.full((n + 256,), 3, dtype=torch.uint8, device="cuda") for n in (n1, n2))
+        assert lib.spec_gated_linear(x.data_ptr(), a.data_ptr(), b.data_ptr(), 1, 3, M, N, K, p["y"], p["g"], p["u"], w1.data_ptr(), n1, st) == 0
+        assert lib.spec_gated_linear_grad(x.data_ptr(), a.data_ptr(), b.data_ptr(), p["g"], p["u"], gy.data_ptr(), 1, 3, M, N, K,
+                                          p["gx"], p["gg"], p["gu"], w2.data_ptr(), n2, st) == 0
+        torch.cuda.synchronize()
+        for k, n in sizes.items():
+            assert (o[k][n:] == 7).all() and (o[k][:n] != 7).any(), k
+        assert (w1[n1:] == 3).all() and (w2[n2:] == 3).all()
+
+
+def test_gated_past_32_bits_of_offset():
+    """An output of more than 2^31 elements, and a weight of as many."""
+    M, N, K = 8400, 262144, 64
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[-1] = 1.0
+    w = torch.ones(N, K, dtype=torch.bfloat16, device="cuda")
+    y = sv.spec_gated_linear(x, w, w, activation=None)
+    assert (y[-1] == K * K).all() and (y[:-1].sum(0) == 0).all()
+    del x, w, y
+    N, K = 262144, 8448
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    w[-1], w[5] = 1.0, 2.0
+    for M in (2, 20):
+        x = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
+        y = sv.spec_gated_linear(x, w, w, activation="relu").float()
+        assert (y[:, -1] == torch.tensor(float(K) ** 2).bfloat16().item()).all() and y.count_nonzero() == 2 * M

@@ -1,0 +1,162 @@
+"""The operators that train a draft head on the host: size queries, and argument
+errors that are found before anything is enqueued.  No kernel is launched."""
+import pytest
+import torch
+
+import draft_verification_row_amd as sv
+import draft_verification_row_amd.markov as mk
+
+OK, EINVAL, EDTYPE, EWORKSPACE = 0, 1, 2, 3
+P = 4096
+WS = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sv.load_library()
+
+
+def test_size_queries(lib):
+    for f in (lib.spec_embedding_grad_workspace_bytes, lib.spec_gated_linear_workspace_bytes,
+              lib.spec_gated_linear_grad_workspace_bytes, lib.spec_cross_entropy_workspace_bytes,
+              lib.spec_cross_entropy_grad_workspace_bytes):
+        assert f(1, 8, 16, 32) > 0 and f(0, 800, 1600, 33) % 256 == 0 and f(0, 800, 1600, 33) > 0
+        for bad in ((2, 8, 16, 32), (-1, 8, 16, 32), (1, 0, 16, 32), (1, 8, 0, 32), (1, 8, 16, 0), (1, -8, 16, 32),
+                    (1, (1 << 20) + 1, 16, 32), (1, 8, (1 << 20) + 1, 32), (1, 8, 16, (1 << 20) + 1),
+                    (1, 8, 1 << 20, 1 << 20), (1, 1 << 20, 8, 1 << 20)):
+            assert f(*bad) == 0, bad
+    # the logits themselves are not in the workspaces
+    assert lib.spec_cross_entropy_workspace_bytes(1, 8192, 128256, 4096) < 8192 * 128256 / 4
+    assert lib.spec_cross_entropy_grad_workspace_bytes(1, 8192, 128256, 4096) < 8192 * 128256
+
+
+def test_embedding_argument_errors(lib):
+    def f(**over):
+        a = dict(w=P, dt=1, tok=P, scale=1.0, n=4, V=8, H=16, y=P, stream=None)
+        a.update(over)
+        return lib.spec_embedding(*a.values())
+
+    need = lib.spec_embedding_grad_workspace_bytes(1, 4, 8, 16)
+
+    def g(**over):
+        a = dict(tok=P, gy=P, dt=1, scale=1.0, n=4, V=8, H=16, gw=P, ws=WS, wsb=need, stream=None)
+        a.update(over)
+        return lib.spec_embedding_grad(*a.values())
+
+    for c in (f, g):
+        assert c(dt=2) == EDTYPE and c(dt=-1) == EDTYPE
+        for bad in (dict(tok=None), dict(n=0), dict(V=0), dict(H=0), dict(n=-3), dict(n=1 << 21), dict(V=1 << 20, H=1 << 15)):
+            assert c(**bad) == EINVAL, bad
+    assert f(w=None) == EINVAL and f(y=None) == EINVAL and g(gy=None) == EINVAL and g(gw=None) == EINVAL
+    assert g(ws=None) == EWORKSPACE and g(ws=WS + 64) == EWORKSPACE and g(wsb=need - 1) == EWORKSPACE
+
+
+def test_gated_argument_errors(lib):
+    need = lib.spec_gated_linear_workspace_bytes(1, 4, 8, 16)
+
+    def f(**over):
+        a = dict(x=P, g=P, u=P, dt=1, act=3, M=4, N=8, K=16, y=P, og=None, ou=None, ws=WS, wsb=need, stream=None)
+        a.update(over)
+        return lib.spec_gated_linear(*a.values())
+
+    gneed = lib.spec_gated_linear_grad_workspace_bytes(1, 4, 8, 16)
+
+    def g(**over):
+        a = dict(x=P, g=P, u=P, pg=P, pu=P, gy=P, dt=1, act=3, M=4, N=8, K=16, gx=P, gg=P, gu=P, ws=WS, wsb=gneed, stream=None)
+        a.update(over)
+        return lib.spec_gated_linear_grad(*a.values())
+
+    for c in (f, g):
+        assert c(dt=2) == EDTYPE
+        for bad in (dict(x=None), dict(g=None), dict(u=None), dict(act=4), dict(act=-1), dict(M=0), dict(N=0), dict(K=0),
+                    dict(M=1 << 21), dict(M=1 << 20, N=1 << 14)):
+            assert c(**bad) == EINVAL, (c.__name__, bad)
+        assert c(ws=None) == EWORKSPACE and c(ws=WS + 64) == EWORKSPACE and c(wsb=0) == EWORKSPACE
+    assert f(y=None) == EINVAL and f(og=P) == EINVAL and f(ou=P) == EINVAL
+    assert g(pg=None) == EINVAL and g(pu=None) == EINVAL and g(gy=None) == EINVAL
+
+
+def test_entropy_argument_errors(lib):
+    need = lib.spec_cross_entropy_workspace_bytes(1, 4, 8, 16)
+
+    def f(**over):
+        a = dict(x=P, w=P, b=None, dt=1, tok=P, M=4, V=8, K=16, loss=P, lse=P, status=P, stats=None, ws=WS, wsb=need, stream=None)
+        a.update(over)
+        return lib.spec_cross_entropy(*a.values())
+
+    gneed = lib.spec_cross_entropy_grad_workspace_bytes(1, 4, 8, 16)
+
+    def g(**over):
+        a = dict(x=P, w=P, b=None, dt=1, tok=P, stats=P, gl=P, ge=None, M=4, V=8, K=16, gx=P, gw=P, gb=P, ws=WS, wsb=gneed, stream=None)
+        a.update(over)
+        return lib.spec_cross_entropy_grad(*a.values())
+
+    for c in (f, g):
+        assert c(dt=2) == EDTYPE
+        for bad in (dict(x=None), dict(w=None), dict(tok=None), dict(M=0), dict(V=0), dict(K=0), dict(V=1 << 21),
+                    dict(M=1 << 20, K=1 << 14)):
+            assert c(**bad) == EINVAL, (c.__name__, bad)
+        assert c(ws=None) == EWORKSPACE and c(ws=WS + 64) == EWORKSPACE and c(wsb=0) == EWORKSPACE
+    assert f(loss=None) == EINVAL and f(lse=None) == EINVAL and f(status=None) == EINVAL and g(stats=None) == EINVAL
+
+
+def test_binding_refuses_host_tensors():
+    X = torch.zeros(2, 50)
+    tok = torch.zeros(2, dtype=torch.int32)
+    for f in (lambda: sv.spec_embedding(X, tok), lambda: sv.spec_gated_linear(X, X, X), lambda: sv.spec_cross_entropy(X, X, tok)):
+        with pytest.raises(sv.SpecVerifyError):
+            f()
+
+
+@pytest.mark.gpu
+def test_binding_refusals():
+    X = torch.zeros(2, 4, 50, device="cuda")
+    W = torch.zeros(30, 50, device="cuda")
+    tok = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    b = torch.zeros(30, device="cuda")
+    E = sv.SpecVerifyError
+    bad = [
+        lambda: sv.spec_embedding(W, tok.long()), lambda: sv.spec_embedding(W.half(), tok), lambda: sv.spec_embedding(W[0], tok),
+        lambda: sv.spec_embedding(W.t(), tok), lambda: sv.spec_embedding(W[:0], tok), lambda: sv.spec_embedding(W, tok.t()),
+        lambda: sv.spec_embedding(W, tok.cpu()), lambda: sv.spec_embedding(W, [1, 2]),
+        lambda: sv.spec_embedding(torch.zeros(1, (1 << 20) + 1, device="cuda"), tok),
+        lambda: sv.spec_gated_linear(X, W, W.bfloat16()), lambda: sv.spec_gated_linear(X.half(), W.half(), W.half()),
+        lambda: sv.spec_gated_linear(X, W, W[:20]), lambda: sv.spec_gated_linear(X, W[:, :40].contiguous(), W),
+        lambda: sv.spec_gated_linear(X, W, W, activation="tanh"), lambda: sv.spec_gated_linear(X.transpose(0, 1), W, W),
+        lambda: sv.spec_gated_linear(X, W[:0], W[:0]), lambda: sv.spec_gated_linear(X, W, W.cpu()),
+        lambda: sv.spec_cross_entropy(X, W, tok.long()), lambda: sv.spec_cross_entropy(X, W, tok[:1]),
+        lambda: sv.spec_cross_entropy(X, W.bfloat16(), tok), lambda: sv.spec_cross_entropy(X, W, tok, b[:20]),
+        lambda: sv.spec_cross_entropy(X, W, tok, b.bfloat16()), lambda: sv.spec_cross_entropy(X, W[:, :40].contiguous(), tok),
+        lambda: sv.spec_cross_entropy(X.half(), W.half(), tok), lambda: sv.spec_cross_entropy(X, W[:0], tok),
+        lambda: sv.spec_cross_entropy(X, W, tok.cpu()),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(E):
+            f()
+            print("not refused:", i)
+
+
+@pytest.mark.gpu
+def test_rows_past_the_limits_are_refused():
+    """2^32 + 3 rows of one element each, which 32 bits take for three."""
+    rows = (1 << 32) + 3
+    one = torch.zeros(rows, 1, dtype=torch.bfloat16, device="cuda")
+    tok = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    w = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda")
+    for f in (lambda: sv.spec_embedding(w, tok), lambda: sv.spec_gated_linear(one, w, w), lambda: sv.spec_cross_entropy(one, w, tok)):
+        with pytest.raises(sv.SpecVerifyError):
+            f()
+
+
+@pytest.mark.gpu
+def test_gated_blocks_of_a_model_are_checked():
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    start, u, v = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.rand(1, 2, 2, device="cuda"), torch.rand(1, 2, 3, device="cuda")
+    good = mk.GatedBlock(z(24, 16), z(24, 16), z(16, 24))
+    m = mk.HeadModel(z(50, 16), [good], z(50, 16))
+    mk.generate_speculative(z(50, 50), m, start, u, v)
+    for i, b in enumerate((good._replace(gate=z(24, 8)), good._replace(up=z(20, 16)), good._replace(down=z(24, 16)),
+                           good._replace(up=z(24, 16).bfloat16()), good._replace(gate=z(24)))):
+        with pytest.raises(sv.SpecVerifyError):
+            mk.generate_speculative(z(50, 50), m._replace(blocks=[b]), start, u, v)
+            print("not refused:", i)
