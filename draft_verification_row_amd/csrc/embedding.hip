@@ -23,7 +23,10 @@ struct Chunk {
             v[j] = __uint_as_float(sizeof(T) == 4 ? q[j % 4] : (j & 1) ? q[j >> 1] & 0xffff0000u : q[j >> 1] << 16);
     }
     __device__ void store(T* row, int k, int len, bool whole, float scale) const {
-        if (whole) {
+        struct Any {
+            u32x4 v;
+        } __attribute__((packed, aligned(sizeof(T))));
+        if (k + kElems <= len) {
             float o[kElems];
 #pragma unroll
             for (int j = 0; j < kElems; ++j) o[j] = v[j] * scale;
@@ -34,7 +37,10 @@ struct Chunk {
                     q[j] = pack_bf16(o[2 * j], o[2 * j + 1]);
                 else
                     q[j] = __float_as_uint(o[j]);
-            __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(row + k));
+            if (whole)
+                __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(row + k));
+            else
+                reinterpret_cast<Any*>(row + k)->v = q;
         } else {
             for (int j = 0; j < kElems && k + j < len; ++j) put(row + k + j, v[j] * scale);
         }
@@ -45,33 +51,42 @@ __device__ inline u32x4 raw_chunk(const T* row, int k, int len, bool whole) {
     return whole ? *reinterpret_cast<const u32x4*>(row + k) : chunk_of(row, k, len);
 }
 
+// How a row is shared out: `lanes` threads a row, a power of two.
+inline int lanes_of(int across) {
+    int lanes = 8;
+    while (lanes < kThreads && lanes < across) lanes *= 2;
+    return lanes;
+}
+
 struct Lookup {
     const void* weight;
     const int32_t* tokens;
-    int64_t chunks;  // of all rows
-    int across;      // chunks a row
-    int V, H;
+    int n, V, H, lanes;
     float scale;
     void* out;
     bool whole;
 };
-// One chunk a thread.  -1: zeros; other tokens outside the table: NaN.
+// -1: zeros; other tokens outside the table: NaN.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_lookup(Lookup a) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= a.chunks) return;
-    const int64_t r = i / a.across;
-    const int k = (int)(i % a.across) * Chunk<T>::kElems, x = a.tokens[r];
-    Chunk<T> c;
-    if (x >= 0 && x < a.V) {
-        c.set(raw_chunk(static_cast<const T*>(a.weight) + (int64_t)x * a.H, k, a.H, a.whole));
-    } else {
+    constexpr int kElems = Chunk<T>::kElems;
+    const int r = blockIdx.x * (kThreads / a.lanes) + threadIdx.x / a.lanes;
+    if (r >= a.n) return;
+    const int x = a.tokens[r];
+    const bool in = x >= 0 && x < a.V;
+    const T* row = static_cast<const T*>(a.weight) + (int64_t)(in ? x : 0) * a.H;
+    T* out = static_cast<T*>(a.out) + (int64_t)r * a.H;
+#pragma unroll 2
+    for (int k = threadIdx.x % a.lanes * kElems; k < a.H; k += a.lanes * kElems) {
+        Chunk<T> c;
+        if (in) {
+            c.set(raw_chunk(row, k, a.H, a.whole));
+        } else {
 #pragma unroll
-        for (int j = 0; j < c.kElems; ++j) c.v[j] = x == -1 ? 0.f : NAN;
-        c.store(static_cast<T*>(a.out) + r * a.H, k, a.H, a.whole, 1.f);
-        return;
+            for (int j = 0; j < kElems; ++j) c.v[j] = x == -1 ? 0.f : NAN;
+        }
+        c.store(out, k, a.H, a.whole, in ? a.scale : 1.f);
     }
-    c.store(static_cast<T*>(a.out) + r * a.H, k, a.H, a.whole, a.scale);
 }
 
 // ------------------------------------------------------------------- sorting
@@ -106,12 +121,13 @@ __global__ __launch_bounds__(64 * kRankWaves) void k_rank(const uint32_t* __rest
 // ------------------------------------------------------------------ gradient
 // Runs of one token longer than kRun are summed in parts: a sorted piece of kRun
 // positions that is all one token has its sum in part [piece][H].
-constexpr int kRun = 64;
+constexpr int kRun = 32;
 struct TableGrad {
     const void* dy;
     const uint32_t* sorted;
     const int* position;
-    int n, V, H, lanes, rows;  // lanes: threads a row; rows: of the table, a workgroup
+    const int* start;
+    int n, V, H, lanes;  // lanes: threads a row
     float* part;
     float scale;
     void* out;
@@ -136,53 +152,80 @@ __global__ __launch_bounds__(kThreads) void k_runs(TableGrad a) {
     }
 }
 
-// the first sorted position whose token is not below x, by the whole workgroup
-__device__ inline int first_of(const uint32_t* sorted, int n, uint32_t x) {
-    int lo = 0, hi = n;  // it is in [lo, hi]
-    while (lo < hi) {
-        const int step = (hi - lo + kThreads - 1) / kThreads, at = lo + (int)threadIdx.x * step;
-        const int below = __syncthreads_count(at < hi && sorted[at] < x);
-        if (below == 0) return lo;
-        const int last = lo + (below - 1) * step;  // is below
-        lo = last + 1;
-        hi = min(hi, last + step);
+// start[v], v in [0, V]: the first sorted position whose token is not below v.
+__global__ __launch_bounds__(kThreads) void k_starts(const uint32_t* sorted, int n, int V, int* start) {
+    const int v = blockIdx.x * kThreads + threadIdx.x;
+    if (v > V) return;
+    int lo = 0;
+    for (int hi = n; lo < hi;) {
+        const int at = (lo + hi) / 2;
+        if (sorted[at] < (uint32_t)v)
+            lo = at + 1;
+        else
+            hi = at;
     }
-    return lo;
+    start[v] = lo;
 }
 
-// A workgroup writes `rows` rows of the table's gradient, `lanes` threads each.
+// A workgroup writes kRowsEach rows of the table's gradient after each other, or
+// that many groups of narrower rows, `lanes` threads a row.
+constexpr int kRowsEach = 8;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_table_grad(TableGrad a) {
+    constexpr int kElems = Chunk<T>::kElems, kAhead = 8;
     const int groups = kThreads / a.lanes, group = threadIdx.x / a.lanes, lane = threadIdx.x % a.lanes;
-    const int64_t v0 = (int64_t)blockIdx.x * a.rows;
-    const int begin = first_of(a.sorted, a.n, (uint32_t)v0), end = first_of(a.sorted, a.n, (uint32_t)min(v0 + a.rows, (int64_t)a.V));
-    for (int64_t v = v0 + group; v < v0 + a.rows && v < a.V; v += groups) {
-        int p = begin;
-        for (int hi = end; p < hi;) {
-            const int at = (p + hi) / 2;
-            if (a.sorted[at] < (uint32_t)v)
-                p = at + 1;
-            else
-                hi = at;
-        }
-        for (int k = lane * Chunk<T>::kElems; k < a.H; k += a.lanes * Chunk<T>::kElems) {
+    const int v0 = blockIdx.x * kRowsEach * groups + group;
+    int from[kRowsEach], to[kRowsEach];
+#pragma unroll
+    for (int i = 0; i < kRowsEach; ++i) {
+        const int v = min(v0 + i * groups, a.V - 1);
+        from[i] = a.start[v];
+        to[i] = a.start[v + 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsEach; ++i) {
+        const int v = v0 + i * groups;
+        if (v >= a.V) break;
+        // whole pieces of the run have their sums already
+        const int first = (from[i] + kRun - 1) / kRun * kRun, last = to[i] / kRun * kRun;
+        const int stop = last > first ? first : to[i], again = last > first ? last : to[i];
+        for (int k = lane * kElems; k < a.H; k += a.lanes * kElems) {
             Chunk<T> sum;
 #pragma unroll
-            for (int j = 0; j < sum.kElems; ++j) sum.v[j] = 0.f;
-            for (int q = p; q < end && a.sorted[q] == (uint32_t)v;) {
-                if (q % kRun == 0 && q + kRun <= end && a.sorted[q + kRun - 1] == (uint32_t)v) {
-                    const float* from = a.part + (int64_t)(q / kRun) * a.H + k;
-                    for (int j = 0; j < sum.kElems && k + j < a.H; ++j) sum.v[j] += from[j];
-                    q += kRun;
-                    continue;
-                }
-                Chunk<T> c;
-                c.set(raw_chunk(static_cast<const T*>(a.dy) + (int64_t)a.position[q] * a.H, k, a.H, a.whole_in));
+            for (int j = 0; j < kElems; ++j) sum.v[j] = 0.f;
+            auto add = [&](int q0, int q1) {
+                for (int q = q0; q < q1; q += kAhead) {
+                    u32x4 raw[kAhead];
 #pragma unroll
-                for (int j = 0; j < c.kElems; ++j) sum.v[j] += c.v[j];
-                ++q;
+                    for (int u = 0; u < kAhead; ++u)
+                        raw[u] = raw_chunk(static_cast<const T*>(a.dy) + (int64_t)a.position[min(q + u, q1 - 1)] * a.H, k, a.H, a.whole_in);
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        if (q + u >= q1) break;
+                        Chunk<T> c;
+                        c.set(raw[u]);
+#pragma unroll
+                        for (int j = 0; j < kElems; ++j) sum.v[j] += c.v[j];
+                    }
+                }
+            };
+            add(from[i], stop);
+            for (int q = first; q < last; q += kRun * kAhead) {
+                float part[kAhead][kElems];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const float* at = a.part + (int64_t)min(q / kRun + u, last / kRun - 1) * a.H + k;
+#pragma unroll
+                    for (int j = 0; j < kElems; ++j) part[u][j] = k + j < a.H ? at[j] : 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (q + u * kRun < last)
+#pragma unroll
+                        for (int j = 0; j < kElems; ++j) sum.v[j] += part[u][j];
             }
-            sum.store(static_cast<T*>(a.out) + v * a.H, k, a.H, a.whole_out, a.scale);
+            add(again, to[i]);
+            sum.store(static_cast<T*>(a.out) + (int64_t)v * a.H, k, a.H, a.whole_out, a.scale);
         }
     }
 }
@@ -195,13 +238,14 @@ inline bool embedding_ok(spec_dtype d, long long n, long long V, long long H) {
            H <= SPEC_MAX_LINEAR && n * H < kMaxTable && V * H < kMaxTable;
 }
 struct EmbeddingLayout {
-    size_t sorted, position, part, total;
+    size_t sorted, position, start, part, total;
 };
-inline EmbeddingLayout embedding_layout(long long n, long long H) {
+inline EmbeddingLayout embedding_layout(long long n, long long V, long long H) {
     EmbeddingLayout l;
     l.sorted = 0;
     l.position = align_up(n * 4, 256);
-    l.part = 2 * l.position;
+    l.start = 2 * l.position;
+    l.part = align_up(l.start + (V + 1) * 4, 256);
     l.total = align_up(l.part + (size_t)(n / kRun * H) * 4, 256);
     return l;
 }
@@ -210,26 +254,27 @@ template <typename T>
 void lookup(const void* weight, const int32_t* tokens, float scale, int n, int V, int H, void* out, hipStream_t st) {
     constexpr int kElems = Chunk<T>::kElems;
     const int across = (H + kElems - 1) / kElems;
-    const int64_t chunks = (int64_t)n * across;
     const bool whole = H % kElems == 0 && ((uintptr_t)weight | (uintptr_t)out) % 16 == 0;
-    k_lookup<T><<<(unsigned)((chunks + kThreads - 1) / kThreads), kThreads, 0, st>>>({weight, tokens, chunks, across, V, H, scale, out, whole});
+    const int lanes = lanes_of(across), rows = kThreads / lanes;
+    k_lookup<T><<<(n + rows - 1) / rows, kThreads, 0, st>>>({weight, tokens, n, V, H, lanes, scale, out, whole});
 }
 
 template <typename T>
 void table_grad(const int32_t* tokens, const void* dy, float scale, int n, int V, int H, void* out, char* ws, hipStream_t st) {
     constexpr int kElems = Chunk<T>::kElems;
-    const EmbeddingLayout lay = embedding_layout(n, H);
+    const EmbeddingLayout lay = embedding_layout(n, V, H);
     uint32_t* sorted = reinterpret_cast<uint32_t*>(ws + lay.sorted);
     int* position = reinterpret_cast<int*>(ws + lay.position);
-    const int across = (H + kElems - 1) / kElems;
-    int lanes = 8;
-    while (lanes < kThreads && lanes < across) lanes *= 2;
+    const int lanes = lanes_of((H + kElems - 1) / kElems);
     const bool whole = H % kElems == 0;
-    const TableGrad g{dy, sorted, position, n, V, H, lanes, 16 * (kThreads / lanes), reinterpret_cast<float*>(ws + lay.part), scale, out,
+    int* start = reinterpret_cast<int*>(ws + lay.start);
+    const TableGrad g{dy, sorted, position, start, n, V, H, lanes, reinterpret_cast<float*>(ws + lay.part), scale, out,
                       whole && (uintptr_t)dy % 16 == 0, whole && (uintptr_t)out % 16 == 0};
     k_rank<<<(n + 63) / 64, 64 * kRankWaves, 0, st>>>(reinterpret_cast<const uint32_t*>(tokens), n, sorted, position);
     if (n >= kRun) k_runs<T><<<n / kRun, kThreads, 0, st>>>(g);
-    k_table_grad<T><<<(V + g.rows - 1) / g.rows, kThreads, 0, st>>>(g);
+    k_starts<<<V / kThreads + 1, kThreads, 0, st>>>(sorted, n, V, start);
+    const int rows = kRowsEach * (kThreads / lanes);
+    k_table_grad<T><<<(V + rows - 1) / rows, kThreads, 0, st>>>(g);
 }
 
 }  // namespace
@@ -247,7 +292,7 @@ extern "C" spec_status spec_embedding(const void* weight, spec_dtype dtype, cons
 }
 
 extern "C" size_t spec_embedding_grad_workspace_bytes(spec_dtype dtype, int n, int V, int H) {
-    return embedding_ok(dtype, n, V, H) ? embedding_layout(n, H).total : 0;
+    return embedding_ok(dtype, n, V, H) ? embedding_layout(n, V, H).total : 0;
 }
 
 extern "C" spec_status spec_embedding_grad(const int32_t* tokens, const void* grad_out, spec_dtype dtype, float scale, int n, int V,
