@@ -5,9 +5,10 @@
 //   dg = dy u act'(g), du = dy act(g)
 //   dx = dg G + du U, dG = dg^T x, dU = du^T x
 // Products are summed in fp32, y is formed from the fp32 sums and rounded once.
-// With bf16 operands the kept g and u and the slopes dg and du are bf16: the
-// slopes are operands of the matrix instructions, and g and u move them by
-// about as much as their own rounding does.
+// With bf16 operands the slopes dg and du are rounded to bf16, as operands of the
+// matrix instructions.  g and u are kept as the fp32 sums: two more roundings to
+// bf16 would put the gradients of 8192 x 14336 x 4096 at 0.0031 from float64
+// instead of 0.0024 (0.0017 is the result's own rounding).
 #include "product.h"
 
 namespace {
@@ -17,7 +18,8 @@ namespace {
 // the same outputs, x is loaded once for both and y needs no second pass.
 template <typename T>
 struct Gate : FromZero {
-    T *y, *g, *u;  // g and u: kept for the gradient, or null
+    T* y;
+    float *g, *u;  // kept for the gradient, or null
     int act;
     bool whole;
     template <class C>
@@ -143,40 +145,34 @@ __global__ __launch_bounds__(kThreads) void k_gated_join(const float* part, int 
 // --------------------------------------------------------------- the slopes
 // dg and du from dy, g and u, rows padded to whole chunks.  Bound by memory.
 struct GateSlope {
-    const void *dy, *g, *u;
+    const void* dy;
+    const float *g, *u;
     void *dg, *du;
     int act, M, N;
     int64_t ld;
-    bool whole;
+    bool whole;  // rows of whole fours, aligned
 };
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_gated_slopes(GateSlope a) {
-    constexpr int kElems = 16 / (int)sizeof(T);
-    const int across = (int)(a.ld / kElems);
+    const int across = (int)(a.ld / 4);
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int m = (int)(i / across), n = (int)(i % across) * kElems;
+    const int m = (int)(i / across), n = (int)(i % across) * 4;
     if (m >= a.M) return;
-    const int64_t at = (int64_t)m * a.N;
-    u32x4 q[3];
-    const T* from[3] = {static_cast<const T*>(a.dy) + at, static_cast<const T*>(a.g) + at, static_cast<const T*>(a.u) + at};
-#pragma unroll
-    for (int k = 0; k < 3; ++k) q[k] = a.whole ? *reinterpret_cast<const u32x4*>(from[k] + n) : chunk_of(from[k], n, a.N);
-    float dg[kElems], du[kElems];
-#pragma unroll
-    for (int j = 0; j < kElems; ++j) {
-        float v[3];
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            v[k] = __uint_as_float(sizeof(T) == 4 ? q[k][j % 4] : (j & 1) ? q[k][j >> 1] & 0xffff0000u : q[k][j >> 1] << 16);
-        dg[j] = v[0] * v[2] * act_slope(v[1], a.act);
-        du[j] = v[0] * act_of(v[1], a.act);
+    const int64_t at = (int64_t)m * a.N + n;
+    const T* dy = static_cast<const T*>(a.dy) + at;
+    float v[4] = {}, g[4] = {}, u[4] = {}, dg[4], du[4];
+    if (a.whole) {
+        if (n < a.N) get4(dy, v), get4(a.g + at, g), get4(a.u + at, u);
+    } else {
+        for (int j = 0; j < 4 && n + j < a.N; ++j) v[j] = to_f(dy[j]), g[j] = a.g[at + j], u[j] = a.u[at + j];
     }
-    T* to[2] = {static_cast<T*>(a.dg) + m * a.ld + n, static_cast<T*>(a.du) + m * a.ld + n};
 #pragma unroll
-    for (int j = 0; j < kElems; j += 4) {
-        put4(to[0] + j, {dg[j], dg[j + 1], dg[j + 2], dg[j + 3]});
-        put4(to[1] + j, {du[j], du[j + 1], du[j + 2], du[j + 3]});
+    for (int j = 0; j < 4; ++j) {
+        dg[j] = v[j] * u[j] * act_slope(g[j], a.act);
+        du[j] = v[j] * act_of(g[j], a.act);
     }
+    put4(static_cast<T*>(a.dg) + m * a.ld + n, dg);
+    put4(static_cast<T*>(a.du) + m * a.ld + n, du);
 }
 
 // ---------------------------------------------------------------- host side
@@ -258,15 +254,13 @@ inline GatedLayout gated_layout(spec_dtype d, long long M, long long N, long lon
 }
 
 template <typename T>
-void gated_backward(const void* x, const void* gate, const void* up, const void* g, const void* u, const void* dy, int act,
+void gated_backward(const void* x, const void* gate, const void* up, const float* g, const float* u, const void* dy, int act,
                     int M, int N, int K, void* gx, void* gg, void* gu, spec_dtype d, char* ws, hipStream_t st) {
     const GatedLayout lay = gated_layout(d, M, N, K);
-    constexpr int kElems = 16 / (int)sizeof(T);
     void *dg = ws + lay.dg, *du = ws + lay.du;
     float* sums = reinterpret_cast<float*>(ws + lay.sums);
-    const bool whole = N % kElems == 0 && ((uintptr_t)g | (uintptr_t)u | (uintptr_t)dy) % 16 == 0;
-    const int64_t chunks = (int64_t)M * (lay.np / kElems);
-    k_gated_slopes<T><<<(unsigned)((chunks + kThreads - 1) / kThreads), kThreads, 0, st>>>({dy, g, u, dg, du, act, M, N, lay.np, whole});
+    const bool whole = fours(g, N, 4) && fours(u, N, 4) && fours(dy, N, sizeof(T));
+    k_gated_slopes<T><<<four_blocks(M, lay.np), kThreads, 0, st>>>({dy, g, u, dg, du, act, M, N, lay.np, whole});
     if (gx) {
         const Product p{{dg, du}, {gate, up}, lay.np, K, M, K, N, N, nullptr, nullptr, 1, lay.split_x};
         if (lay.split_x > 1) {
@@ -303,20 +297,19 @@ extern "C" size_t spec_gated_linear_workspace_bytes(spec_dtype dtype, int M, int
 }
 
 extern "C" spec_status spec_gated_linear(const void* x, const void* gate, const void* up, spec_dtype dtype,
-                                         spec_activation activation, int M, int N, int K, void* out, void* out_gate,
-                                         void* out_up, void* workspace, size_t workspace_bytes, void* stream) {
+                                         spec_activation activation, int M, int N, int K, void* out, float* out_gate,
+                                         float* out_up, void* workspace, size_t workspace_bytes, void* stream) {
     if (!type_ok(dtype)) return SPEC_EDTYPE;
     if (!gated_ok(dtype, M, N, K) || !act_ok(activation) || !x || !gate || !up || !out || !out_gate != !out_up) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_gated_linear_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
     const Product g{{x, x}, {gate, up}, K, K, M, N, K, 0, nullptr, nullptr, 1, 1};
-    const size_t four = 4 * elem(dtype);
-    const bool whole = N % 4 == 0 && ((uintptr_t)out | (uintptr_t)out_gate | (uintptr_t)out_up) % four == 0;
+    const bool whole = fours(out, N, elem(dtype)) && fours(out_gate, N, 4) && fours(out_up, N, 4);
     char* ws = static_cast<char*>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (value_of(dtype) == SPEC_BF16)
-        gated_forward(g, Gate<bf16>{{}, (bf16*)out, (bf16*)out_gate, (bf16*)out_up, activation, whole}, dtype, ws, st);
+        gated_forward(g, Gate<bf16>{{}, (bf16*)out, out_gate, out_up, activation, whole}, dtype, ws, st);
     else
-        gated_forward(g, Gate<float>{{}, (float*)out, (float*)out_gate, (float*)out_up, activation, whole}, dtype, ws, st);
+        gated_forward(g, Gate<float>{{}, (float*)out, out_gate, out_up, activation, whole}, dtype, ws, st);
     return launched();
 }
 
@@ -324,8 +317,8 @@ extern "C" size_t spec_gated_linear_grad_workspace_bytes(spec_dtype dtype, int M
     return gated_ok(dtype, M, N, K) ? gated_layout(dtype, M, N, K).total : 0;
 }
 
-extern "C" spec_status spec_gated_linear_grad(const void* x, const void* gate, const void* up, const void* gate_preact,
-                                              const void* up_preact, const void* grad_out, spec_dtype dtype,
+extern "C" spec_status spec_gated_linear_grad(const void* x, const void* gate, const void* up, const float* gate_preact,
+                                              const float* up_preact, const void* grad_out, spec_dtype dtype,
                                               spec_activation activation, int M, int N, int K, void* grad_x, void* grad_gate,
                                               void* grad_up, void* workspace, size_t workspace_bytes, void* stream) {
     if (!type_ok(dtype)) return SPEC_EDTYPE;

@@ -96,7 +96,7 @@ def _gated(x, gate, up, act, keep):
     N, K = gate.shape
     M = x.numel() // K
     out = torch.empty((*x.shape[:-1], N), dtype=x.dtype, device=x.device)
-    g, u = ((torch.empty((M, N), dtype=x.dtype, device=x.device) for _ in range(2)) if keep
+    g, u = ((torch.empty((M, N), dtype=torch.float32, device=x.device) for _ in range(2)) if keep
             else (None, None))
     if M:
         code = _dtype_code(x)
@@ -145,7 +145,7 @@ def spec_gated_linear(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, *,
 
     x [..., K], gate and up [N][K] in one dtype, bfloat16 or float32; the
     result [..., N] too.  activation as spec_linear's.  Every tensor input has
-    a gradient; for it both products are kept in the inputs' dtype.
+    a gradient; for it both products are kept in float32.
     """
     _check(x, "x")
     _dtype_code(x)

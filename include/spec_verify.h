@@ -630,7 +630,7 @@ spec_status spec_embedding_grad(const int32_t *tokens, const void *grad_out, spe
  * They are summed in fp32, y is formed from the sums and rounded once.
  *
  *   x [M][K], gate (G), up (U) [N][K], out [M][N]     dtype
- *   out_gate, out_up [M][N] dtype, or both NULL: x G^T and x U^T, which the
+ *   out_gate, out_up [M][N] float, or both NULL: x G^T and x U^T, which the
  *                gradients need
  * Any activation of spec_linear.  1 <= M, N, K <= SPEC_MAX_LINEAR, and M * N,
  * M * K and N * K below 2^33.  The workspaces need no initialization and are
@@ -639,16 +639,17 @@ spec_status spec_embedding_grad(const int32_t *tokens, const void *grad_out, spe
 size_t spec_gated_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K);
 spec_status spec_gated_linear(const void *x, const void *gate, const void *up, spec_dtype dtype,
                               spec_activation activation, int M, int N, int K, void *out,
-                              void *out_gate, void *out_up, void *workspace,
+                              float *out_gate, float *out_up, void *workspace,
                               size_t workspace_bytes, void *stream);
 
 /* Its gradients: with dg = grad_out up_preact act'(gate_preact) and du =
  * grad_out act(gate_preact), both rounded to dtype, grad_x = dg G + du U,
  * grad_gate = dg^T x and grad_up = du^T x.  A NULL output is not computed;
- * gate and up are read for grad_x, x for the others.  Everything in dtype. */
+ * gate and up are read for grad_x, x for the others.  All but the preacts in
+ * dtype. */
 size_t spec_gated_linear_grad_workspace_bytes(spec_dtype dtype, int M, int N, int K);
 spec_status spec_gated_linear_grad(const void *x, const void *gate, const void *up,
-                                   const void *gate_preact, const void *up_preact,
+                                   const float *gate_preact, const float *up_preact,
                                    const void *grad_out, spec_dtype dtype,
                                    spec_activation activation, int M, int N, int K, void *grad_x,
                                    void *grad_gate, void *grad_up, void *workspace,
