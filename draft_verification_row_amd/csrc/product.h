@@ -159,14 +159,14 @@ __global__ __launch_bounds__(kThreads, C::kStageBytes * C::STAGES <= 80 * 1024 ?
     // row r of W's part of a stage: which matrix of a pair, and its column n
     auto pair_of = [](int r) { return C::PAIR && r % C::WN >= C::kWaveN; };
     auto col_of = [](int r) { return C::PAIR ? r / C::WN * C::kWaveN + r % C::kWaveN : r; };
-    auto x_at = [&](int s) {
-        const int i = g.products == 2 ? product : second(s);
-        return static_cast<const T*>(g.x[i]) + (C::XK ? (int64_t)k_of(s) * g.ldx + m0 : m0 * g.ldx + k_of(s));
-    };
-    auto w_at = [&](int s, bool other) {
-        const int i = C::PAIR ? other : second(s);
-        return static_cast<const T*>(g.w[i]) + (C::WK ? (int64_t)k_of(s) * g.ldw + n0 : n0 * g.ldw + k_of(s));
-    };
+    // both sums' operands from this tile's first row and column on
+    const int64_t xm = C::XK ? m0 : m0 * g.ldx, wn0 = C::WK ? n0 : n0 * g.ldw;
+    const T* const x1 = static_cast<const T*>(product ? g.x[1] : g.x[0]) + xm;
+    const T* const x2 = static_cast<const T*>(g.x[1]) + xm;
+    const T* const w1 = static_cast<const T*>(g.w[0]) + wn0;
+    const T* const w2 = static_cast<const T*>(g.w[1]) + wn0;
+    auto x_at = [&](int s) { return (second(s) ? x2 : x1) + (C::XK ? k_of(s) * g.ldx : k_of(s)); };
+    auto w_at = [&](int s, bool other) { return ((C::PAIR ? other : second(s)) ? w2 : w1) + (C::WK ? k_of(s) * g.ldw : k_of(s)); };
 
     // offsets of this lane's loads; what lies past the matrix reads a row or
     // column that does not: those sums are dropped
