@@ -348,6 +348,196 @@ __global__ __launch_bounds__(kThreads, C::kStageBytes * C::STAGES <= 80 * 1024 ?
     e.template finish<C>(part, acc);
 }
 
+// ------------------------------------------------------------- the large tile
+// 256 x 256 outputs of four waves, 128 x 128 each, one wave a SIMD: nothing but
+// its own order hides what a wave waits for.  A stage is four quarters of 128
+// rows each, the first and the second halves of every wave's rows of X (A0, A1)
+// and of W (B0, B1); in a pair, B0 is the one matrix and B1 the other.  A stage's
+// products go by quadrants, A0 B0, A0 B1, A1 B1, A1 B0, each quarter read to
+// registers once, under the quadrant before its first: so a quarter's place in
+// LDS is free half a stage or more before the stage ends, its next loads go out
+// evenly over the whole of the stage, and each has at least a stage's time
+// (2048 cycles) to arrive.
+template <class C, class E>
+__global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
+    using T = typename C::T;
+    static_assert(C::BM == 256 && C::BN == 256 && C::WM == 128 && C::WN == 128 && C::DIRECT, "the large tile");
+    using LX = Lies<T, 128, C::XK>;
+    using LW = Lies<T, 128, C::WK>;
+    constexpr int kElems = C::kElems, kStep = C::kStep, kQuarter = 128 * 128, kLoads = 16;
+    enum { A0, B0, B1, A1 };  // in the order of their loads
+    __shared__ __attribute__((aligned(1024))) char lds[2][4 * kQuarter];
+    const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int M = g.live_m ? __builtin_amdgcn_readfirstlane(*g.live_m) : g.M;
+    const int K = g.live_k ? __builtin_amdgcn_readfirstlane(*g.live_k) : g.K;
+    const unsigned tiles_m = (M + 255) / 256, tiles_n = (g.N + C::kColsN - 1) / C::kColsN, tiles = tiles_m * tiles_n;
+    if (blockIdx.x >= tiles * (unsigned)(g.splits * g.products)) return;
+    const int turn = blockIdx.x / tiles, split = turn % g.splits, product = turn / g.splits;
+    int tm, tn;
+    tile_of(blockIdx.x % tiles, tiles, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * 256, n0 = tn * C::kColsN;
+
+    // the order of the sum's steps, as in k_product
+    const int whole1 = K / kStep, whole = whole1 + g.K2 / kStep;
+    const int rest1 = K % kStep != 0, steps = whole + rest1 + (g.K2 % kStep != 0);
+    const int per = (steps + g.splits - 1) / g.splits, begin = split * per, end = min(steps, begin + per);
+    auto second = [&](int s) { return s < whole ? s >= whole1 : s >= whole + rest1; };
+    auto k_of = [&](int s) {
+        if (s < whole) return (s < whole1 ? s : s - whole1) * kStep;
+        return (second(s) ? g.K2 : K) / kStep * kStep;
+    };
+    // row r of a quarter of X or W among the tile's rows
+    auto row_x = [](int q, int r) { return r / 64 * 128 + (q == A1) * 64 + r % 64; };
+    auto row_w = [](int q, int r) { return C::PAIR ? r : r / 64 * 128 + (q == B1) * 64 + r % 64; };
+    const int64_t xm = C::XK ? m0 : m0 * g.ldx, wn = C::WK ? n0 : n0 * g.ldw;
+    const T* const x1 = static_cast<const T*>(product ? g.x[1] : g.x[0]) + xm;
+    const T* const x2 = static_cast<const T*>(g.x[1]) + xm;
+    const T* const w1 = static_cast<const T*>(g.w[0]) + wn;
+    const T* const w2 = static_cast<const T*>(g.w[1]) + wn;
+    auto from = [&](int q, int s) -> const T* {
+        if (q == A0 || q == A1) return (second(s) ? x2 : x1) + (C::XK ? k_of(s) * g.ldx : k_of(s));
+        return ((C::PAIR ? q == B1 : second(s)) ? w2 : w1) + (C::WK ? k_of(s) * g.ldw : k_of(s));
+    };
+
+    // offsets of this lane's loads, four a quarter; what lies past the matrix
+    // reads a row or column that does not: those sums are dropped
+    uint32_t off[kLoads];
+    each(std::make_integer_sequence<int, kLoads>(), [&](auto i) {
+        constexpr int q = i / 4, u = i % 4;
+        int64_t at;
+        if constexpr (q == A0 || q == A1) {
+            const int r = LX::row(u, w, lane), c = LX::chunk(u, w, lane) * kElems;
+            if constexpr (C::XK)
+                at = r * g.ldx + (row_x(q, c) < M - m0 ? row_x(q, c) : 0);
+            else
+                at = min(row_x(q, r), M - 1 - m0) * g.ldx + c;
+        } else {
+            const int r = LW::row(u, w, lane), c = LW::chunk(u, w, lane) * kElems;
+            if constexpr (C::WK)
+                at = r * g.ldw + (row_w(q, c) < g.N - n0 ? row_w(q, c) : 0);
+            else
+                at = min(row_w(q, r), g.N - 1 - n0) * g.ldw + c;
+        }
+        off[i] = (uint32_t)(at * (int64_t)sizeof(T));
+    });
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)&lds[0][0] + w * 1024;
+    const int stop = min(end, whole);
+    // a whole step's buffers; past the last step they have no length, and their
+    // loads nothing to load
+    struct Buffers {
+        __amdgpu_buffer_rsrc_t x, w, p;
+    };
+    auto buffers = [&](int s) -> Buffers {
+        const bool sec = s >= whole1;
+        const int64_t k = (int64_t)(sec ? s - whole1 : s) * kStep;
+        auto rsrc = [&](const T* p) { return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), (short)0, s < stop ? 0x7fffffff : 0, 0x00020000); };
+        const int64_t kx = C::XK ? k * g.ldx : k, kw = C::WK ? k * g.ldw : k;
+        if constexpr (C::PAIR) return {rsrc(x1 + kx), rsrc(w1 + kw), rsrc(w2 + kw)};
+        const __amdgpu_buffer_rsrc_t w = rsrc((sec ? w2 : w1) + kw);
+        return {rsrc((sec ? x2 : x1) + kx), w, w};
+    };
+    auto load = [&](int slot, auto i, const Buffers& f) {
+        constexpr int q = i / 4;
+        to_lds<i * 4096, false>(q == A0 || q == A1 ? f.x : q == B0 ? f.w : f.p, lds0 + slot * 4 * kQuarter, off[i], 0);
+    };
+
+    const Part part{m0 + w / 2 * 128, n0 + w % 2 * C::kWaveN, M, g.N, lane, w, tm, tn, split, product, &lds[0][0]};
+    f32x16 acc[4][4] = {};
+    e.template start<C>(part, acc);
+    // A quarter's operands: two blocks, four pairs of chunks.  b2: the next B0,
+    // read while b0 is still in use.
+    u32x4 a0[8], a1[8], b0[8], b1[8], b2[8];
+    auto read = [&](int slot, int q, int i, u32x4 (&o)[8]) {
+        const char* at = &lds[slot][q * kQuarter];
+        if (q == A0 || q == A1)
+            o[i] = operand<T, 128, C::XK>(at, i / 2, w / 2 * 64 + i % 2 * 32, lane);
+        else
+            o[i] = operand<T, 128, C::WK>(at, i / 2, w % 2 * 64 + i % 2 * 32, lane);
+    };
+    // A quadrant's sixteen products, `between` called before each.
+    auto quadrant = [&](auto i0, auto j0, const u32x4 (&wq)[8], const u32x4 (&xq)[8], auto&& between) {
+        each(std::make_integer_sequence<int, 16>(), [&](auto u) {
+            between(u);
+            constexpr int p = u / 4, i = u / 2 % 2, j = u % 2;
+            acc[i0 + i][j0 + j] = mfma32(T(), wq[p * 2 + i], xq[p * 2 + j], acc[i0 + i][j0 + j]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    using Zero = std::integral_constant<int, 0>;
+    using Two = std::integral_constant<int, 2>;
+    auto arrived = [&](auto left) {  // all but the last `left` loads, in every wave; and every wave has read what it asked for
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"((int)left) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    int s = begin;
+    if (s < stop) {
+        each(std::make_integer_sequence<int, kLoads>(), [&](auto i) { load(0, i, buffers(s)); });
+        each(std::make_integer_sequence<int, kLoads>(), [&](auto i) { load(1, i, buffers(s + 1)); });
+        arrived(std::integral_constant<int, 24>());
+#pragma unroll
+        for (int i = 0; i < 8; ++i) read(0, A0, i, a0), read(0, B0, i, b2);
+        int slot = 0;
+        // a stage: step s + 2 is loaded into its place, a load every fourth product
+        do {
+            using Left = std::integral_constant<int, kLoads>;
+            const Buffers f = buffers(s + 2);
+            arrived(Left());
+            quadrant(Zero(), Zero(), b2, a0, [&](auto u) {
+                if constexpr (u % 2 == 0) read(slot, B1, u / 2, b1);
+                if constexpr (u % 2 == 1) b0[u / 2] = b2[u / 2];
+                if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, u / 4>(), f);
+            });
+            quadrant(Two(), Zero(), b1, a0, [&](auto u) {
+                if constexpr (u < 8) read(slot, A1, u, a1);
+                if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, 4 + u / 4>(), f);
+            });
+            arrived(Left());
+            const int other = 1 - slot;
+            quadrant(Two(), Two(), b1, a1, [&](auto u) {
+                if constexpr (u % 2 == 0) read(other, A0, u / 2, a0);
+                if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, 8 + u / 4>(), f);
+            });
+            quadrant(Zero(), Two(), b0, a1, [&](auto u) {
+                if constexpr (u < 8) read(other, B0, u, b2);
+                if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, 12 + u / 4>(), f);
+            });
+            slot = other;
+        } while (++s < stop);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    // what is no whole step, through registers, zero past the sum's end
+    for (; s < end; ++s) {
+        const int left = (second(s) ? g.K2 : K) - k_of(s);
+        u32x4 v[kLoads];
+        each(std::make_integer_sequence<int, kLoads>(), [&](auto i) {
+            constexpr int q = i / 4, u = i % 4;
+            constexpr bool x = q == A0 || q == A1;
+            const int r = x ? LX::row(u, w, lane) : LW::row(u, w, lane), c = (x ? LX::chunk(u, w, lane) : LW::chunk(u, w, lane)) * kElems;
+            const int64_t ld = x ? g.ldx : g.ldw;
+            const int rows = x ? M - m0 : g.N - n0;
+            const T* p = from(q, s);
+            v[i] = (u32x4){0, 0, 0, 0};
+            if (x ? C::XK : C::WK) {
+                if (r < left) v[i] = chunk_of(p + r * ld, x ? row_x(q, c) : row_w(q, c), rows);
+            } else {
+                v[i] = chunk_of(p + min(x ? row_x(q, r) : row_w(q, r), rows - 1) * ld, c, left);
+            }
+        });
+        __syncthreads();
+        each(std::make_integer_sequence<int, kLoads>(), [&](auto i) { *reinterpret_cast<u32x4*>(&lds[0][i * 4096 + w * 1024 + lane * 16]) = v[i]; });
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) read(0, A0, i, a0), read(0, B0, i, b0), read(0, B1, i, b1), read(0, A1, i, a1);
+        quadrant(Zero(), Zero(), b0, a0, [](auto) {});
+        quadrant(Two(), Zero(), b1, a0, [](auto) {});
+        quadrant(Two(), Two(), b1, a1, [](auto) {});
+        quadrant(Zero(), Two(), b0, a1, [](auto) {});
+    }
+    __syncthreads();
+    e.template finish<C>(part, acc);
+}
+
 // ------------------------------------------------------------- plain epilogue
 struct FromZero {
     template <class C>
@@ -443,7 +633,10 @@ template <class C, class E>
 void launch_tile(const Product& g, const E& e, hipStream_t st) {
     const unsigned grid = (unsigned)((g.M + C::BM - 1) / C::BM) * (unsigned)((g.N + C::kColsN - 1) / C::kColsN) *
                           (unsigned)(g.splits * g.products);
-    k_product<C, E><<<grid, kThreads, 0, st>>>(g, e);
+    if constexpr (C::BM == 256)
+        k_wide<C, E><<<grid, kThreads, 0, st>>>(g, e);
+    else
+        k_product<C, E><<<grid, kThreads, 0, st>>>(g, e);
 }
 inline bool aligned(const Product& g, size_t e) {
     uintptr_t a = (uintptr_t)g.x[0] | (uintptr_t)g.w[0] | (uintptr_t)g.x[1] | (uintptr_t)g.w[1];
