@@ -22,10 +22,27 @@ __device__ inline float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog
 // --------------------------------------------------------------- rows in use
 // Rows of padded tokens are left out of the products: live[i] is the i-th row
 // in use and place[r] its number i, -1 where row r is not in use.
+struct Outputs {
+    float *loss, *lse, *stats;
+    int32_t* status;
+};
+// Outputs of a row whose token is x, if it is not in use; returns whether it is.
+__device__ inline bool in_use(const Outputs& o, int64_t r, int x, int V) {
+    const bool in = x >= 0 && x < V;
+    if (o.status) {
+        o.status[r] = x < -1 || x >= V;
+        if (!in) {
+            o.loss[r] = o.lse[r] = 0.f;
+            if (o.stats) o.stats[2 * r] = o.stats[2 * r + 1] = 0.f;
+        }
+    }
+    return in;
+}
 struct Rows {
     const int32_t* tokens;
     int M, V;
     int *live, *place, *count;
+    Outputs out;  // forward
 };
 constexpr int kLiveThreads = 1024;
 __global__ __launch_bounds__(kLiveThreads) void k_live(Rows a) {
@@ -33,8 +50,8 @@ __global__ __launch_bounds__(kLiveThreads) void k_live(Rows a) {
     const int t = threadIdx.x, lane = t & 63, w = t >> 6;
     int before = 0;
     for (int r0 = 0; r0 < a.M; r0 += kLiveThreads) {
-        const int r = r0 + t, x = r < a.M ? a.tokens[r] : -1;
-        const bool in = x >= 0 && x < a.V;
+        const int r = r0 + t;
+        const bool in = r < a.M && in_use(a.out, r, a.tokens[r], a.V);
         const uint64_t mask = __ballot(in);
         if (lane == 0) waves[w] = __popcll(mask);
         __syncthreads();
@@ -74,11 +91,11 @@ __device__ inline MaxSum joined(MaxSum a, MaxSum b) {
     return {top, a.sum * exp_of(a.top - ref) + b.sum * exp_of(b.top - ref)};
 }
 
-// f(value) for a lane's values of the j-th 32 rows.
+// f(value) for a lane's values of the j-th kB rows.
 template <class C, class J, typename F>
-__device__ __attribute__((always_inline)) inline void values(f32x16 (&acc)[C::FN][C::FM], J j, F f) {
-    each(std::make_integer_sequence<int, C::FN * 16>(), [&](auto u) __attribute__((always_inline)) {
-        constexpr int i = u / 16, v = u % 16;
+__device__ __attribute__((always_inline)) inline void values(typename C::Acc (&acc)[C::FN][C::FM], J j, F f) {
+    each(std::make_integer_sequence<int, C::FN * C::kV>(), [&](auto u) __attribute__((always_inline)) {
+        constexpr int i = u / C::kV, v = u % C::kV;
         acc[i][j][v] = f(acc[i][j][v]);
     });
 }
@@ -87,11 +104,11 @@ template <typename T>
 struct Logits {
     const T* bias;  // or null
     template <class C>
-    __device__ __attribute__((always_inline)) void start(const Part& p, f32x16 (&acc)[C::FN][C::FM]) const {
+    __device__ __attribute__((always_inline)) void start(const Part& p, typename C::Acc (&acc)[C::FN][C::FM]) const {
         if (!bias && p.n0 + C::WN <= p.N) return;
-        each(std::make_integer_sequence<int, C::FN * 16>(), [&](auto u) __attribute__((always_inline)) {
-            constexpr int i = u / 16, v = u % 16;
-            const int n = p.n0 + i * 32 + v / 4 * 8 + (p.lane >> 5) * 4 + v % 4;
+        each(std::make_integer_sequence<int, C::FN * C::kV>(), [&](auto u) __attribute__((always_inline)) {
+            constexpr int i = u / C::kV, v = u % C::kV;
+            const int n = p.n0 + i * C::kB + v / 4 * 8 + p.lane / C::kB * 4 + v % 4;
             const float b = n >= p.N ? -INFINITY : bias ? to_f(bias[n]) : 0.f;
 #pragma unroll
             for (int j = 0; j < C::FM; ++j) acc[i][j][v] = b;
@@ -110,28 +127,31 @@ struct Stats : Logits<T> {
     MaxSum* part;
     float* picked;
     template <class C>
-    __device__ __attribute__((always_inline)) void finish(const Part& p, f32x16 (&acc)[C::FN][C::FM]) const {
-        const int l = p.lane & 31, h = p.lane >> 5;
+    __device__ __attribute__((always_inline)) void finish(const Part& p, typename C::Acc (&acc)[C::FN][C::FM]) const {
+        const int l = p.lane % C::kB;
+        const bool first = p.lane < C::kB;  // of the lanes that share a row
         MaxSum* red = reinterpret_cast<MaxSum*>(p.lds);
         MaxSum all[C::FM];
         each(std::make_integer_sequence<int, C::FM>(), [&](auto j) __attribute__((always_inline)) {
-            const int m = p.m0 + j * 32 + l;
+            const int m = p.m0 + j * C::kB + l;
             float top = -INFINITY, sum = 0.f;
             values<C>(acc, j, [&](float z) __attribute__((always_inline)) { return top = fmaxf(top, z), z; });
             const float ref = top == -INFINITY ? 0.f : top;
             values<C>(acc, j, [&](float z) __attribute__((always_inline)) { return sum += exp_of(z - ref), z; });
-            all[j] = joined({top, sum}, {__shfl_xor(top, 32), __shfl_xor(sum, 32)});
+            all[j] = {top, sum};
+#pragma unroll
+            for (int s = C::kB; s < 64; s *= 2) all[j] = joined(all[j], {__shfl_xor(all[j].top, s), __shfl_xor(all[j].sum, s)});
             const int x = m < p.M ? tokens[live ? live[m] : m] - p.n0 : -1;
             const bool here = x >= 0 && x < C::WN && p.n0 + x < p.N;
             if (__ballot(here) == 0) return;
-            lay<C>(p, acc, j);
-            if (here && h == 0) picked[m] = rows_of<C>(p)[l * (C::WN + 4) + x];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            lay<C>(p, acc, std::integral_constant<int, j * C::kB / 32>());
+            if (here && first) picked[m] = rows_of<C>(p)[(j * C::kB % 32 + l) * (C::WN + 4) + x];
+            settle();
         });
         __syncthreads();
-        if (h == 0)
+        if (first)
 #pragma unroll
-            for (int j = 0; j < C::FM; ++j) red[p.w % C::kWavesN * C::BM + p.w / C::kWavesN * C::WM + j * 32 + l] = all[j];
+            for (int j = 0; j < C::FM; ++j) red[p.w % C::kWavesN * C::BM + p.w / C::kWavesN * C::WM + j * C::kB + l] = all[j];
         __syncthreads();
         const int t = threadIdx.x, m = p.tm * C::BM + t;
         if (t < C::BM && m < p.M) {
@@ -152,7 +172,7 @@ struct Fold {
     const int32_t* tokens;
     const int *live, *count;  // or null: every row
     int M, V, parts, across;
-    float *loss, *lse, *stats;
+    Outputs out;
 };
 __global__ __launch_bounds__(kLiveThreads) void k_fold(Fold a) {
     __shared__ MaxSum red[kLiveThreads];
@@ -170,27 +190,17 @@ __global__ __launch_bounds__(kLiveThreads) void k_fold(Fold a) {
     }
     if (g != 0 || m >= rows) return;
     v = red[t];
-    const int r = a.live ? a.live[m] : m, x = a.tokens[r];
-    if (x < 0 || x >= a.V) return;
+    const int64_t r = a.live ? a.live[m] : m;
+    const Outputs& o = a.out;
+    if (!in_use(o, r, a.tokens[r], a.V)) return;
     const bool some = v.top != -INFINITY || v.sum != v.sum;
     const float ls = logf(v.sum);
-    a.loss[r] = some ? ls - (a.picked[m] - v.top) : INFINITY;
-    a.lse[r] = some ? v.top + ls : -INFINITY;
-    if (a.stats) {
-        a.stats[2 * (int64_t)r] = some ? v.top : 0.f;
-        a.stats[2 * (int64_t)r + 1] = some ? 1.f / v.sum : 0.f;
+    o.loss[r] = some ? ls - (a.picked[m] - v.top) : INFINITY;
+    o.lse[r] = some ? v.top + ls : -INFINITY;
+    if (o.stats) {
+        o.stats[2 * r] = some ? v.top : 0.f;
+        o.stats[2 * r + 1] = some ? 1.f / v.sum : 0.f;
     }
-}
-
-// Outputs of padded rows, and every row's status.
-__global__ __launch_bounds__(kThreads) void k_padded(const int32_t* tokens, int M, int V, float* loss, float* lse, int32_t* status, float* stats) {
-    const int r = blockIdx.x * kThreads + threadIdx.x;
-    if (r >= M) return;
-    const int x = tokens[r];
-    status[r] = x < -1 || x >= V;
-    if (x >= 0 && x < V) return;
-    loss[r] = lse[r] = 0.f;
-    if (stats) stats[2 * (int64_t)r] = stats[2 * (int64_t)r + 1] = 0.f;
 }
 
 // ------------------------------------------------------------------ backward
@@ -206,31 +216,40 @@ struct Slope : Logits<T> {  // the bias: of the piece
     int64_t ld;
     float* part;  // or null
     template <class C>
-    __device__ __attribute__((always_inline)) void finish(const Part& p, f32x16 (&acc)[C::FN][C::FM]) const {
-        const int l = p.lane & 31, h = p.lane >> 5;
+    __device__ __attribute__((always_inline)) void finish(const Part& p, typename C::Acc (&acc)[C::FN][C::FM]) const {
+        const int l = p.lane % C::kB;
+        const bool first = p.lane < C::kB;  // of the lanes that share a row
         constexpr int kLanes = C::WN / 4, kAtOnce = 64 / kLanes, kPitch = C::WN + 4;
         const int c = p.lane % kLanes * 4, n = p.n0 + c;
         float sum[4] = {};
-        each(std::make_integer_sequence<int, C::FM>(), [&](auto j) __attribute__((always_inline)) {
-            const int m = p.m0 + j * 32 + l;
-            float top = 0.f, inv = 0.f, one = 0.f, both = 0.f;
-            int x = -1;
-            if (m < p.M) {
-                const int r = live[m];
-                top = stats[2 * (int64_t)r], inv = stats[2 * (int64_t)r + 1];
-                one = g_loss && inv != 0.f ? g_loss[r] : 0.f;
-                both = one + (g_lse ? g_lse[r] : 0.f);
-                x = tokens[r] - v0 - p.n0;
-            }
-            values<C>(acc, j, [&](float z) __attribute__((always_inline)) {
-                // p from the difference itself; 0 whatever the weight where p = 0
-                const float q = exp_of(z - top) * inv;
-                return q == 0.f ? 0.f : both * q;
+        each(std::make_integer_sequence<int, C::WM / 32>(), [&](auto j) __attribute__((always_inline)) {
+            constexpr int kBlocks = 32 / C::kB;
+            int at[kBlocks];
+            float minus[kBlocks];
+            each(std::make_integer_sequence<int, kBlocks>(), [&](auto k) __attribute__((always_inline)) {
+                const int m = p.m0 + j * 32 + k * C::kB + l;
+                float top = 0.f, inv = 0.f, one = 0.f, both = 0.f;
+                at[k] = -1;
+                if (m < p.M) {
+                    const int r = live[m];
+                    top = stats[2 * (int64_t)r], inv = stats[2 * (int64_t)r + 1];
+                    one = g_loss && inv != 0.f ? g_loss[r] : 0.f;
+                    both = one + (g_lse ? g_lse[r] : 0.f);
+                    at[k] = tokens[r] - v0 - p.n0;
+                }
+                minus[k] = one;
+                values<C>(acc, std::integral_constant<int, j * kBlocks + k>(), [&](float z) __attribute__((always_inline)) {
+                    // p from the difference itself; 0 whatever the weight where p = 0
+                    const float q = exp_of(z - top) * inv;
+                    return q == 0.f ? 0.f : both * q;
+                });
             });
             lay<C>(p, acc, j);
             float* rows = rows_of<C>(p);
-            if (h == 0 && x >= 0 && x < C::WN) rows[l * kPitch + x] -= one;
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int k = 0; k < kBlocks; ++k)
+                if (first && at[k] >= 0 && at[k] < C::WN) rows[(k * C::kB + l) * kPitch + at[k]] -= minus[k];
+            settle();
             if (n < p.N)
 #pragma unroll 4
                 for (int r = p.lane / kLanes; r < 32; r += kAtOnce) {
@@ -242,7 +261,7 @@ struct Slope : Logits<T> {  // the bias: of the piece
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sum[i] += q[i];
                 }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            settle();
         });
         if (!part) return;
 #pragma unroll
@@ -282,12 +301,12 @@ inline bool entropy_ok(spec_dtype d, long long M, long long V, long long K) {
 
 // The product that gives logits.  Up to 64 rows take tiles of all of them by
 // 128 of W, which read W once and past the caches.
-enum Shape { kRows32, kRows64, kLogits256, kLogits128, kLogits64 };
-inline Shape shape_of(long long M, long long V) {
+enum Shape { kRows32, kRows64, kRows192, kLogits256, kLogits128, kLogits64 };
+inline Shape shape_of(spec_dtype d, long long M, long long V, long long K) {
     if (M <= 32) return kRows32;
     if (M <= 64) return kRows64;
-    const Size s = size_of(M, V, 1);
-    return s == kTile256 ? kLogits256 : s == kTile128 ? kLogits128 : kLogits64;
+    const Size s = plan_of(d, M, V, K, 1, false, true).size;
+    return s == kTile192 ? kRows192 : s == kTile256 ? kLogits256 : s == kTile128 ? kLogits128 : kLogits64;
 }
 // Where W's rows are no whole chunks, they are copied to padded ones first if
 // more than 64 rows use them.
@@ -297,7 +316,7 @@ struct Tiling {
 };
 inline Tiling tiling(Shape s, bool direct) {
     if (!direct || s == kLogits64) return {64, 64, 2};
-    return s == kRows32 ? Tiling{32, 128, 1} : s == kRows64 ? Tiling{64, 128, 1} : s == kLogits256 ? Tiling{256, 256, 2} : Tiling{128, 128, 2};
+    return s == kRows32 ? Tiling{32, 128, 1} : s == kRows64 ? Tiling{64, 128, 1} : s == kRows192 ? Tiling{192, 128, 2} : s == kLogits256 ? Tiling{256, 256, 2} : Tiling{128, 128, 2};
 }
 template <typename T, class E>
 void launch_logits(const Product& g, const E& e, Shape s, hipStream_t st) {
@@ -307,6 +326,8 @@ void launch_logits(const Product& g, const E& e, Shape s, hipStream_t st) {
         launch_tile<Tile<T, 32, 128, 32, 32, 4, false, false, false, true, true>>(g, e, st);
     else if (s == kRows64)
         launch_tile<Tile<T, 64, 128, 64, 32, 3, false, false, false, true, true>>(g, e, st);
+    else if (s == kRows192)
+        launch_tile<Tile<T, 192, 128, 96, 64, 3, false, false, false, true>>(g, e, st);
     else
         launch_product<T, false, false>(g, e, s == kLogits256 ? kTile256 : s == kLogits128 ? kTile128 : kTile64, st);
 }
@@ -345,12 +366,12 @@ void entropy_forward(const void* x, const void* weight, const void* bias, const 
     const int64_t ld = padded(d, K);
     MaxSum* part = reinterpret_cast<MaxSum*>(ws + lay.part);
     float* picked = reinterpret_cast<float*>(ws + lay.picked);
-    Product g{{x, x}, {weight, weight}, K, K, M, V, K, 0, nullptr, nullptr, 1, 1};
-    k_padded<<<(M + kThreads - 1) / kThreads, kThreads, 0, st>>>(tokens, M, V, loss, lse, status, stats);
+    Product g{{x, x}, {weight, weight}, K, K, M, V, K, 0, nullptr, nullptr, 1, 1, 0};
+    const Outputs out{loss, lse, stats, status};
     if (lay.few) {
         live = count = nullptr;
     } else {
-        k_live<<<1, kLiveThreads, 0, st>>>({tokens, M, V, live, reinterpret_cast<int*>(ws + lay.place), count});
+        k_live<<<1, kLiveThreads, 0, st>>>({tokens, M, V, live, reinterpret_cast<int*>(ws + lay.place), count, out});
         pack<T>(x, live, count, M, K, ld, ws + lay.x, st);
         g.x[0] = g.x[1] = ws + lay.x;
         g.ldx = ld;
@@ -362,12 +383,12 @@ void entropy_forward(const void* x, const void* weight, const void* bias, const 
             g.K = (int)ld;  // the padding is zero
         }
     }
-    const Shape s = shape_of(M, V);
+    const Shape s = shape_of(d, M, V, K);
     launch_logits<T>(g, Stats<T>{{static_cast<const T*>(bias)}, tokens, live, M, part, picked}, s, st);
     const int bn = tiling(s, aligned(g, sizeof(T))).bn;
     int across = 1;
     while (across < M && across < 64) across *= 2;
-    k_fold<<<(M + across - 1) / across, kLiveThreads, 0, st>>>({part, picked, tokens, live, count, M, V, (V + bn - 1) / bn, across, loss, lse, stats});
+    k_fold<<<(M + across - 1) / across, kLiveThreads, 0, st>>>({part, picked, tokens, live, count, M, V, (V + bn - 1) / bn, across, out});
 }
 
 // A piece of the vocabulary: what keeps its dz within kPieceBytes.
@@ -378,15 +399,19 @@ inline int piece_of(spec_dtype d, long long M, long long V) {
 }
 struct BackwardLayout {
     size_t live, place, count, x, w, dz, dx, dw, part, total;
-    int piece, split_x, split_w;
+    int piece, more;  // more: splits of dx where few rows are in use
+    Plan px, pw;
     bool packs;
 };
 inline BackwardLayout backward_layout(spec_dtype d, long long M, long long V, long long K) {
     BackwardLayout l;
     l.piece = piece_of(d, M, V);
     l.packs = packs_weight(d, M, K);
-    l.split_x = splits_at(d, M, K, l.piece, 1);
-    l.split_w = splits_at(d, l.piece, K, M, 1);
+    l.px = plan_of(d, M, K, l.piece, 1, true, false);
+    l.pw = plan_of(d, l.piece, K, M, 1, true, false);
+    // room for up to four times the compute units' tiles
+    const long long b = 256 >> l.px.size, tiles = ((M + b - 1) / b) * ((K + b - 1) / b), most = 1024 / tiles;
+    l.more = (int)(most > kMaxSplits ? kMaxSplits : most < l.px.splits ? l.px.splits : most);
     l.live = 0;
     l.place = align_up(l.live + M * 4, 256);
     l.count = align_up(l.place + M * 4, 256);
@@ -394,8 +419,8 @@ inline BackwardLayout backward_layout(spec_dtype d, long long M, long long V, lo
     l.w = l.x + matrix_bytes(d, M, padded(d, K));
     l.dz = l.w + (l.packs ? matrix_bytes(d, V, padded(d, K)) : 0);
     l.dx = l.dz + matrix_bytes(d, M, padded(d, l.piece));
-    l.dw = align_up(l.dx + (size_t)(l.split_x * M * K) * 4, 256);
-    l.part = align_up(l.dw + (l.split_w > 1 ? (size_t)l.split_w * l.piece * K * 4 : 0), 256);
+    l.dw = align_up(l.dx + (size_t)(l.more * M * K) * 4, 256);
+    l.part = align_up(l.dw + (l.pw.splits > 1 ? (size_t)l.pw.splits * l.piece * K * 4 : 0), 256);
     l.total = align_up(l.part + (size_t)((M + 31) / 32 * V) * 4, 256);
     return l;
 }
@@ -414,7 +439,7 @@ void entropy_backward(const void* x, const void* weight, const void* bias, const
     float* part = gb ? reinterpret_cast<float*>(ws + lay.part) : nullptr;
     int64_t ldw = K;
     int kz = K;
-    k_live<<<1, kLiveThreads, 0, st>>>({tokens, M, V, live, place, count});
+    k_live<<<1, kLiveThreads, 0, st>>>({tokens, M, V, live, place, count, {}});
     pack<T>(x, live, count, M, K, ld, ws + lay.x, st);
     if (lay.packs) {
         pack<T>(weight, nullptr, nullptr, V, K, ld, ws + lay.w, st);
@@ -422,31 +447,33 @@ void entropy_backward(const void* x, const void* weight, const void* bias, const
         ldw = ld;
         kz = (int)ld;
     }
-    const Shape shape = shape_of(M, lay.piece);
+    const Shape shape = shape_of(d, M, lay.piece, K);
     const int64_t ldz = padded(d, lay.piece);
     Tiling tiles{};
+    int dx_tile = 64;
     for (int v0 = 0; v0 < V; v0 += lay.piece) {
         const int n = V - v0 < lay.piece ? V - v0 : lay.piece;
         const T* w = wp + v0 * ldw;
-        const Product z{{xp, xp}, {w, w}, ld, ldw, M, n, kz, 0, count, nullptr, 1, 1};
+        const Product z{{xp, xp}, {w, w}, ld, ldw, M, n, kz, 0, count, nullptr, 1, 1, 0};
         tiles = tiling(shape, aligned(z, sizeof(T)));
         launch_logits<T>(z, Slope<T>{{bias ? static_cast<const T*>(bias) + v0 : nullptr}, tokens, live, stats, g_loss, g_lse, v0, V, dz, ldz, part}, shape, st);
         if (gx) {
-            const Product p{{dz, dz}, {w, w}, ldz, ldw, M, K, n, 0, count, nullptr, 1, lay.split_x};
-            launch_product<T, false, true>(p, Store<float>{{}, {dx, dx}, K, (int64_t)M * K, v0 > 0, fours(dx, K, 4)}, size_of(M, K, 1), st);
+            const Product p{{dz, dz}, {w, w}, ldz, ldw, M, K, n, 0, count, nullptr, 1, lay.px.splits, lay.more};
+            dx_tile = aligned(p, sizeof(T)) ? 256 >> lay.px.size : 64;
+            launch_product<T, false, true>(p, Store<float>{{}, {dx, dx}, K, (int64_t)M * K, v0 > 0, fours(dx, K, 4)}, lay.px.size, st);
         }
         if (gw) {
             T* out = static_cast<T*>(gw) + (int64_t)v0 * K;
-            const Product p{{dz, dz}, {xp, xp}, ldz, ld, n, K, M, 0, nullptr, count, 1, lay.split_w};
-            if (lay.split_w > 1) {
-                launch_product<T, true, true>(p, Store<float>{{}, {dw, dw}, K, (int64_t)n * K, false, fours(dw, K, 4)}, kTile64, st);
-                k_join<T><<<four_blocks(n, K), kThreads, 0, st>>>(dw, lay.split_w, (int64_t)n * K, nullptr, n, K, out);
+            const Product p{{dz, dz}, {xp, xp}, ldz, ld, n, K, M, 0, nullptr, count, 1, lay.pw.splits, 0};
+            if (lay.pw.splits > 1) {
+                launch_product<T, true, true>(p, Store<float>{{}, {dw, dw}, K, (int64_t)n * K, false, fours(dw, K, 4)}, lay.pw.size, st);
+                join(dw, lay.pw.splits, nullptr, {}, n, K, out, st);
             } else {
-                launch_product<T, true, true>(p, Store<T>{{}, {out, out}, K, 0, false, fours(out, K, sizeof(T))}, size_of(lay.piece, K, 1), st);
+                launch_product<T, true, true>(p, Store<T>{{}, {out, out}, K, 0, false, fours(out, K, sizeof(T))}, lay.pw.size, st);
             }
         }
     }
-    if (gx) k_join<T><<<four_blocks(M, K), kThreads, 0, st>>>(dx, lay.split_x, (int64_t)M * K, place, M, K, static_cast<T*>(gx));
+    if (gx) join(dx, lay.px.splits, place, {count, dx_tile, lay.more}, M, K, static_cast<T*>(gx), st);
     if (gb) k_bias_fold<T><<<(V + 63) / 64, kLiveThreads, 0, st>>>(part, count, tiles.bm, tiles.waves_m, V, static_cast<T*>(gb));
 }
 

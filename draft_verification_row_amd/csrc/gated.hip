@@ -23,7 +23,7 @@ struct Gate : FromZero {
     int act;
     bool whole;
     template <class C>
-    __device__ __attribute__((always_inline)) void finish(const Part& p, f32x16 (&acc)[C::FN][C::FM]) const {
+    __device__ __attribute__((always_inline)) void finish(const Part& p, typename C::Acc (&acc)[C::FN][C::FM]) const {
         constexpr int kLanes = C::kWaveN / 4, kAtOnce = 64 / kLanes, kPitch = C::WN + 4;
         const int c = p.lane % kLanes * 4, n = p.n0 + c;
         turned<C>(p, acc, [&](int j, float* rows) __attribute__((always_inline)) {
@@ -182,25 +182,44 @@ inline bool gated_ok(spec_dtype d, long long M, long long N, long long K) {
            K <= SPEC_MAX_LINEAR && M * N < (1ll << 33) && M * K < (1ll << 33) && N * K < (1ll << 33);
 }
 
-// Rows whose length is no whole number of chunks are copied to padded ones for
-// the larger tiles, which load straight to LDS.
+// Rows whose length is no whole number of chunks are copied to padded ones where
+// more than 16 rows of x use them, so that tiles are loaded straight to LDS.
 inline size_t packed_bytes(spec_dtype d, long long rows, long long k) { return align_up((size_t)(rows * padded(d, k)) * elem(d), 256); }
-inline bool packs_pair(spec_dtype d, long long M, long long N, long long K) {
-    return padded(d, K) != K && M > 16 && size_of(M, 2 * N, 1) != kTile64;
+inline bool packs_pair(spec_dtype d, long long M, long long K) {
+    return padded(d, K) != K && M > 16;
 }
+struct Pads {
+    const void* from[3];
+    void* to[3];
+    int64_t end[3];  // rows up to the end of each
+};
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_pad_rows(const T* from, int64_t rows, int K, int64_t ld, T* to) {
+__global__ __launch_bounds__(kThreads) void k_pad_rows(Pads a, int K, int64_t ld) {
     constexpr int kElems = 16 / (int)sizeof(T);
     const int64_t across = ld / kElems, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t m = i / across;
-    if (m >= rows) return;
-    const int k = (int)(i % across) * kElems;
-    *reinterpret_cast<u32x4*>(to + m * ld + k) = chunk_of(from + m * K, k, K);
+    int64_t m = i / across;
+    if (m >= a.end[2]) return;
+    const int which = m >= a.end[1] ? 2 : m >= a.end[0], k = (int)(i % across) * kElems;
+    if (which) m -= a.end[which - 1];
+    *reinterpret_cast<u32x4*>(static_cast<T*>(a.to[which]) + m * ld + k) = chunk_of(static_cast<const T*>(a.from[which]) + m * K, k, K);
 }
+// x, gate and up, those that are asked for (else null), padded into ws one after
+// the other; returns where they are
+struct Padded {
+    const void *x, *gate, *up;
+    int64_t ld;
+};
 template <typename T>
-void pad_rows(const void* from, long long rows, int K, int64_t ld, void* to, hipStream_t st) {
-    const int64_t n = rows * (ld / (16 / (int64_t)sizeof(T)));
-    k_pad_rows<T><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(static_cast<const T*>(from), rows, K, ld, static_cast<T*>(to));
+Padded pad_rows(const void* x, const void* gate, const void* up, spec_dtype d, int M, int N, int K, char* ws, hipStream_t st) {
+    const int64_t ld = padded(d, K);
+    char *px = ws, *pg = px + packed_bytes(d, M, K), *pu = pg + packed_bytes(d, N, K);
+    Pads a{{x, gate, up}, {px, pg, pu}, {}};
+    a.end[0] = x ? M : 0;
+    a.end[1] = a.end[0] + (gate ? N : 0);
+    a.end[2] = a.end[1] + (up ? N : 0);
+    const int64_t n = a.end[2] * (ld / (16 / (int64_t)sizeof(T)));
+    if (n) k_pad_rows<T><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(a, K, ld);
+    return {px, pg, pu, ld};
 }
 
 template <typename T>
@@ -213,21 +232,19 @@ void gated_forward(Product g, const Gate<T>& e, spec_dtype d, char* ws, hipStrea
             k_gated_few<T, false><<<grid, kThreads, 0, st>>>(g, e);
         return;
     }
-    if (packs_pair(d, g.M, g.N, g.K)) {
-        const int64_t ld = padded(d, g.K);
-        char *x = ws, *a = x + packed_bytes(d, g.M, g.K), *b = a + packed_bytes(d, g.N, g.K);
-        pad_rows<T>(g.x[0], g.M, g.K, ld, x, st);
-        pad_rows<T>(g.w[0], g.N, g.K, ld, a, st);
-        pad_rows<T>(g.w[1], g.N, g.K, ld, b, st);
-        g.x[0] = x, g.w[0] = a, g.w[1] = b;
-        g.ldx = g.ldw = ld;
-        g.K = (int)ld;  // the padding is zero
+    if (packs_pair(d, g.M, g.K)) {
+        const Padded p = pad_rows<T>(g.x[0], g.w[0], g.w[1], d, g.M, g.N, g.K, ws, st);
+        g.x[0] = g.x[1] = p.x, g.w[0] = p.gate, g.w[1] = p.up;
+        g.ldx = g.ldw = p.ld;
+        g.K = (int)p.ld;  // the padding is zero
     }
-    const Size size = size_of(g.M, 2ll * g.N, 1);
+    const Size size = plan_of(d, g.M, 2ll * g.N, g.K, 1, false, true).size;
     if (!aligned(g, sizeof(T)))
         launch_tile<Tile<T, 64, 128, 32, 64, 2, false, false, true, false>>(g, e, st);
     else if (size == kTile256)
         launch_tile<Tile<T, 256, 256, 128, 128, 2, false, false, true, true>>(g, e, st);
+    else if (size == kTile192)
+        launch_tile<Tile<T, 192, 128, 96, 64, 3, false, false, true, true>>(g, e, st);
     else if (size == kTile128)
         launch_tile<Tile<T, 128, 128, 64, 64, 4, false, false, true, true>>(g, e, st);
     else
@@ -237,18 +254,19 @@ void gated_forward(Product g, const Gate<T>& e, spec_dtype d, char* ws, hipStrea
 // The gradients' workspace: dg and du, and the sums of split products.
 struct GatedLayout {
     int64_t np;
-    size_t dg, du, sums, total;
-    int split_x, split_w;
+    size_t dg, du, packed, sums, total;
+    Plan x, w;
 };
 inline GatedLayout gated_layout(spec_dtype d, long long M, long long N, long long K) {
     GatedLayout l;
     l.np = padded(d, N);
     l.dg = 0;
     l.du = align_up((size_t)(M * l.np) * elem(d), 256);
-    l.sums = 2 * l.du;
-    l.split_x = splits_at(d, M, K, 2 * N, 1);
-    l.split_w = splits_at(d, N, K, M, 2);
-    const size_t a = l.split_x > 1 ? (size_t)(l.split_x * M * K) * 4 : 0, b = l.split_w > 1 ? (size_t)(2 * l.split_w * N * K) * 4 : 0;
+    l.packed = 2 * l.du;
+    l.sums = l.packed + (packs_pair(d, M, K) ? packed_bytes(d, M, K) + 2 * packed_bytes(d, N, K) : 0);
+    l.x = plan_of(d, M, K, 2 * N, 1, true, false);
+    l.w = plan_of(d, N, K, M, 2, true, false);
+    const size_t a = l.x.splits > 1 ? (size_t)(l.x.splits * M * K) * 4 : 0, b = l.w.splits > 1 ? (size_t)(2 * l.w.splits * N * K) * 4 : 0;
     l.total = l.sums + align_up(a > b ? a : b, 256);
     return l;
 }
@@ -261,13 +279,18 @@ void gated_backward(const void* x, const void* gate, const void* up, const float
     float* sums = reinterpret_cast<float*>(ws + lay.sums);
     const bool whole = fours(g, N, 4) && fours(u, N, 4) && fours(dy, N, sizeof(T));
     k_gated_slopes<T><<<four_blocks(M, lay.np), kThreads, 0, st>>>({dy, g, u, dg, du, act, M, N, lay.np, whole});
+    int64_t ld = K;
+    if (packs_pair(d, M, K)) {
+        const Padded p = pad_rows<T>(gg || gu ? x : nullptr, gx ? gate : nullptr, gx ? up : nullptr, d, M, N, K, ws + lay.packed, st);
+        x = p.x, gate = p.gate, up = p.up, ld = p.ld;
+    }
     if (gx) {
-        const Product p{{dg, du}, {gate, up}, lay.np, K, M, K, N, N, nullptr, nullptr, 1, lay.split_x};
-        if (lay.split_x > 1) {
-            launch_product<T, false, true>(p, Store<float>{{}, {sums, sums}, K, (int64_t)M * K, false, fours(sums, K, 4)}, kTile64, st);
-            k_join<T><<<four_blocks(M, K), kThreads, 0, st>>>(sums, lay.split_x, (int64_t)M * K, nullptr, M, K, static_cast<T*>(gx));
+        const Product p{{dg, du}, {gate, up}, lay.np, ld, M, K, N, N, nullptr, nullptr, 1, lay.x.splits, 0};
+        if (lay.x.splits > 1) {
+            launch_product<T, false, true>(p, Store<float>{{}, {sums, sums}, K, (int64_t)M * K, false, fours(sums, K, 4)}, lay.x.size, st);
+            join(sums, lay.x.splits, nullptr, {}, M, K, static_cast<T*>(gx), st);
         } else {
-            launch_product<T, false, true>(p, Store<T>{{}, {static_cast<T*>(gx), static_cast<T*>(gx)}, K, 0, false, fours(gx, K, sizeof(T))}, size_of(M, K, 1), st);
+            launch_product<T, false, true>(p, Store<T>{{}, {static_cast<T*>(gx), static_cast<T*>(gx)}, K, 0, false, fours(gx, K, sizeof(T))}, lay.x.size, st);
         }
     }
     if (gg || gu) {
@@ -275,16 +298,16 @@ void gated_backward(const void* x, const void* gate, const void* up, const float
         const void *a = gg ? dg : du, *b = gu ? du : dg;
         T *oa = static_cast<T*>(gg ? gg : gu), *ob = static_cast<T*>(gu ? gu : gg);
         const int products = gg && gu ? 2 : 1;
-        const Product p{{a, b}, {x, x}, lay.np, K, N, K, M, 0, nullptr, nullptr, products, lay.split_w};
-        if (lay.split_w > 1) {
+        const Product p{{a, b}, {x, x}, lay.np, ld, N, K, M, 0, nullptr, nullptr, products, lay.w.splits, 0};
+        if (lay.w.splits > 1) {
             const int64_t one = (int64_t)N * K;
-            float* second = sums + lay.split_w * one;
-            launch_product<T, true, true>(p, Store<float>{{}, {sums, second}, K, one, false, fours(sums, K, 4)}, kTile64, st);
-            k_join<T><<<four_blocks(N, K), kThreads, 0, st>>>(sums, lay.split_w, one, nullptr, N, K, oa);
-            if (products == 2) k_join<T><<<four_blocks(N, K), kThreads, 0, st>>>(second, lay.split_w, one, nullptr, N, K, ob);
+            float* second = sums + lay.w.splits * one;
+            launch_product<T, true, true>(p, Store<float>{{}, {sums, second}, K, one, false, fours(sums, K, 4)}, lay.w.size, st);
+            join(sums, lay.w.splits, nullptr, {}, N, K, oa, st);
+            if (products == 2) join(second, lay.w.splits, nullptr, {}, N, K, ob, st);
         } else {
             const bool four = fours(oa, K, sizeof(T)) && fours(ob, K, sizeof(T));
-            launch_product<T, true, true>(p, Store<T>{{}, {oa, ob}, K, 0, false, four}, size_of(N, K, 2), st);
+            launch_product<T, true, true>(p, Store<T>{{}, {oa, ob}, K, 0, false, four}, lay.w.size, st);
         }
     }
 }
@@ -293,7 +316,7 @@ void gated_backward(const void* x, const void* gate, const void* up, const float
 
 extern "C" size_t spec_gated_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K) {
     if (!gated_ok(dtype, M, N, K)) return 0;
-    return packs_pair(dtype, M, N, K) ? packed_bytes(dtype, M, K) + 2 * packed_bytes(dtype, N, K) : 256;
+    return packs_pair(dtype, M, K) ? packed_bytes(dtype, M, K) + 2 * packed_bytes(dtype, N, K) : 256;
 }
 
 extern "C" spec_status spec_gated_linear(const void* x, const void* gate, const void* up, spec_dtype dtype,
@@ -302,7 +325,7 @@ extern "C" spec_status spec_gated_linear(const void* x, const void* gate, const 
     if (!type_ok(dtype)) return SPEC_EDTYPE;
     if (!gated_ok(dtype, M, N, K) || !act_ok(activation) || !x || !gate || !up || !out || !out_gate != !out_up) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_gated_linear_workspace_bytes(dtype, M, N, K))) return SPEC_EWORKSPACE;
-    const Product g{{x, x}, {gate, up}, K, K, M, N, K, 0, nullptr, nullptr, 1, 1};
+    const Product g{{x, x}, {gate, up}, K, K, M, N, K, 0, nullptr, nullptr, 1, 1, 0};
     const bool whole = fours(out, N, elem(dtype)) && fours(out_gate, N, 4) && fours(out_up, N, 4);
     char* ws = static_cast<char*>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);

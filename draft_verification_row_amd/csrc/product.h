@@ -17,7 +17,14 @@ struct Product {
     const int *live_m, *live_k;  // on the device: the count that stands for M, or for K, or null
     int products;             // 1, or 2: x[0] and x[1] with the same w
     int splits;               // of the sum over k
+    int more;                 // with live_m: splits where few rows are in use, or 0
 };
+// The splits where `tiles` of a workgroup each are in use: enough of them for a
+// compute unit each, as far as there is room for their sums.
+__host__ __device__ inline int splits_in_use(int splits, int more, unsigned tiles) {
+    const int want = tiles ? (int)(256 / tiles) : 1;
+    return want <= splits ? splits : want < more ? want : more > splits ? more : splits;
+}
 
 // One tile's shape.  XK, WK: the operand lies by k.  PAIR: w[0] and w[1] are
 // multiplied side by side, BN / 2 rows of each, every wave with the same rows of
@@ -29,7 +36,10 @@ struct Tile {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
     static constexpr bool XK = XK_, WK = WK_, PAIR = PAIR_, DIRECT = DIRECT_, ONCE = ONCE_;
     static constexpr int kElems = 16 / (int)sizeof(T), kStep = 8 * kElems;  // k of a stage: 128 bytes of a row
-    static constexpr int FM = WM / 32, FN = WN / 32, kWavesM = BM / WM, kWavesN = BN / WN;
+    // a block of the result and of the matrix instructions: kB x kB
+    static constexpr int kB = BM == 256 && sizeof(T) == 2 ? 16 : 32, kV = kB * kB / 64;
+    using Acc = std::conditional_t<kB == 16, f32x4, f32x16>;  // a lane's kV values of one
+    static constexpr int FM = WM / kB, FN = WN / kB, kWavesM = BM / WM, kWavesN = BN / WN;
     static constexpr int kColsN = PAIR ? BN / 2 : BN;  // columns of the result
     static constexpr int kWaveN = PAIR ? WN / 2 : WN;
     static constexpr int kStageBytes = (BM + BN) * 128;
@@ -41,9 +51,10 @@ struct Tile {
 // after k of B elements.  A load is 1 KiB, lane after lane 16 bytes.  Chunks
 // are exchanged within their row so that the reads of an instruction's operand
 // use each bank once: by rows, sixteen rows are read at one chunk; by k in
-// bf16, four k of 64 neighbouring bytes at once; in fp32, 128 bytes of two k
-// that are four apart.
-template <typename T, int B, bool K>
+// bf16, four k of 64 neighbouring bytes at once, or (SIXTEEN) four and four k
+// that are eight apart of 32 bytes; in fp32, 128 bytes of two k that are four
+// apart.
+template <typename T, int B, bool K, bool SIXTEEN = false>
 struct Lies {
     static constexpr int kRowBytes = K ? B * (int)sizeof(T) : 128, kRowChunks = kRowBytes / 16;
     static constexpr int kRows = 64 / kRowChunks, kLoads = B / 32;
@@ -51,7 +62,7 @@ struct Lies {
     __device__ static int row(int i, int w, int lane) { return (i * 4 + w) * kRows + lane / kRowChunks; }
     __device__ static int swizzle(int r) {
         if constexpr (!K) return r >> 1 & 7;
-        else if constexpr (sizeof(T) == 2) return kRowBytes >= 256 ? (r & 3) << 2 : kRowBytes == 128 ? (r >> 1 & 1) << 2 : 0;
+        else if constexpr (sizeof(T) == 2) return SIXTEEN ? ((r & 3) | (r >> 3 & 1) << 2) << 1 : kRowBytes >= 256 ? (r & 3) << 2 : kRowBytes == 128 ? (r >> 1 & 1) << 2 : 0;
         else return kRowBytes >= 256 ? (r >> 2 & 1) << 3 : 0;
     }
     __device__ static int chunk(int i, int w, int lane) { return lane % kRowChunks ^ swizzle(row(i, w, lane)); }
@@ -85,6 +96,24 @@ __device__ inline u32x4 operand(const char* at, int pair, int r0, int lane) {
     }
 }
 
+// The same of 16 rows, for a bf16 instruction of 32 k: lane l has row r0 + l % 16
+// and chunk 4 step + l / 16.
+template <int B, bool K>
+__device__ inline u32x4 operand16(const char* at, int step, int r0, int lane) {
+    using L = Lies<bf16, B, K, true>;
+    const int l = lane & 15, h = lane >> 4;
+    if constexpr (!K) {
+        return *reinterpret_cast<const u32x4*>(at + (r0 + l) * 128 + ((4 * step + h) ^ L::swizzle(l)) * 16);
+    } else {
+        const int k = h * 8 + (l >> 2);
+        const char* p = at + (step * 32 + k) * L::kRowBytes + (r0 * 2 ^ L::swizzle(k) * 16) + (l & 3) * 8;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p + 4 * L::kRowBytes));
+        const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+        return (u32x4){x[0], x[1], y[0], y[1]};
+    }
+}
+
 // Where a wave's part of the result lies.
 struct Part {
     int m0, n0;       // its first row and column
@@ -95,6 +124,14 @@ struct Part {
     char* lds;        // the workgroup's, free to use
 };
 
+// What the wave's lanes wrote to the LDS is there for all of them.  The barrier
+// emits nothing, but keeps the lanes together: without it the compiler may let
+// those that skip the reads run ahead to the next writes.
+__device__ __attribute__((always_inline)) inline void settle() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A wave's blocks of the j-th 32 rows of m, laid in its own part of the LDS so
 // that neighbouring lanes may take neighbouring n: row r at rows + r * (WN + 4).
 template <class C>
@@ -103,28 +140,29 @@ __device__ inline float* rows_of(const Part& p) {
     return reinterpret_cast<float*>(p.lds) + p.w * 32 * (C::WN + 4);
 }
 template <class C, class J>
-__device__ __attribute__((always_inline)) inline void lay(const Part& p, f32x16 (&acc)[C::FN][C::FM], J j) {
-    float* rows = rows_of<C>(p) + (p.lane & 31) * (C::WN + 4) + (p.lane >> 5) * 4;
-    each(std::make_integer_sequence<int, C::FN * 4>(), [&](auto u) __attribute__((always_inline)) {
-        constexpr int i = u / 4, q = u % 4;
-        *reinterpret_cast<f32x4*>(rows + i * 32 + q * 8) =
-            (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+__device__ __attribute__((always_inline)) inline void lay(const Part& p, typename C::Acc (&acc)[C::FN][C::FM], J j) {
+    constexpr int kFours = C::kV / 4, kBlocks = 32 / C::kB;
+    float* rows = rows_of<C>(p) + p.lane % C::kB * (C::WN + 4) + p.lane / C::kB * 4;
+    each(std::make_integer_sequence<int, kBlocks * C::FN * kFours>(), [&](auto u) __attribute__((always_inline)) {
+        constexpr int k = u / (C::FN * kFours), i = u / kFours % C::FN, q = u % kFours, jj = j * kBlocks + k;
+        *reinterpret_cast<f32x4*>(rows + k * C::kB * (C::WN + 4) + i * C::kB + q * 8) =
+            (f32x4){acc[i][jj][4 * q], acc[i][jj][4 * q + 1], acc[i][jj][4 * q + 2], acc[i][jj][4 * q + 3]};
     });
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    settle();
 }
 // All of them in turn: f(j, rows).
 template <class C, typename F>
-__device__ __attribute__((always_inline)) inline void turned(const Part& p, f32x16 (&acc)[C::FN][C::FM], F f) {
-    each(std::make_integer_sequence<int, C::FM>(), [&](auto j) __attribute__((always_inline)) {
+__device__ __attribute__((always_inline)) inline void turned(const Part& p, typename C::Acc (&acc)[C::FN][C::FM], F f) {
+    each(std::make_integer_sequence<int, C::WM / 32>(), [&](auto j) __attribute__((always_inline)) {
         lay<C>(p, acc, j);
         f(j, rows_of<C>(p));
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        settle();
     });
 }
 
 // The product.  E::start<C>(part, acc) may set what the sums start from, and
-// E::finish<C>(part, acc) takes each wave's sums: acc[i][j] is a 32 x 32 block,
-// lane l with row l % 32 of m, value 4 q + r with column 8 q + 4 (l / 32) + r of
+// E::finish<C>(part, acc) takes each wave's sums: acc[i][j] is a block of kB x kB,
+// lane l with row l % kB of m, value 4 q + r with column 8 q + 4 (l / kB) + r of
 // n.
 template <class C, class E>
 __global__ __launch_bounds__(kThreads, C::kStageBytes * C::STAGES <= 80 * 1024 ? 2 : 1) void k_product(Product g, E e) {
@@ -139,8 +177,9 @@ __global__ __launch_bounds__(kThreads, C::kStageBytes * C::STAGES <= 80 * 1024 ?
     const int M = g.live_m ? __builtin_amdgcn_readfirstlane(*g.live_m) : g.M;
     const int K = g.live_k ? __builtin_amdgcn_readfirstlane(*g.live_k) : g.K;
     const unsigned tiles_m = (M + BM - 1) / BM, tiles_n = (g.N + C::kColsN - 1) / C::kColsN, tiles = tiles_m * tiles_n;
-    if (blockIdx.x >= tiles * (unsigned)(g.splits * g.products)) return;
-    const int turn = blockIdx.x / tiles, split = turn % g.splits, product = turn / g.splits;
+    const int splits = splits_in_use(g.splits, g.more, tiles);
+    if (blockIdx.x >= tiles * (unsigned)(splits * g.products)) return;
+    const int turn = blockIdx.x / tiles, split = turn % splits, product = turn / splits;
     int tm, tn;
     tile_of(blockIdx.x % tiles, tiles, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * C::kColsN;
@@ -150,7 +189,7 @@ __global__ __launch_bounds__(kThreads, C::kStageBytes * C::STAGES <= 80 * 1024 ?
     // left of each.  This split's are [begin, end).
     const int whole1 = K / kStep, whole = whole1 + g.K2 / kStep;
     const int rest1 = K % kStep != 0, steps = whole + rest1 + (g.K2 % kStep != 0);
-    const int per = (steps + g.splits - 1) / g.splits, begin = split * per, end = min(steps, begin + per);
+    const int per = (steps + splits - 1) / splits, begin = split * per, end = min(steps, begin + per);
     auto second = [&](int s) { return s < whole ? s >= whole1 : s >= whole + rest1; };
     auto k_of = [&](int s) {
         if (s < whole) return (s < whole1 ? s : s - whole1) * kStep;
@@ -231,7 +270,7 @@ __global__ __launch_bounds__(kThreads, C::kStageBytes * C::STAGES <= 80 * 1024 ?
     };
 
     const Part part{m0 + wm, n0 + w % C::kWavesN * C::kWaveN, M, g.N, lane, w, tm, tn, split, product, &lds[0][0]};
-    f32x16 acc[FN][FM] = {};
+    typename C::Acc acc[FN][FM] = {};
     e.template start<C>(part, acc);
     // Operands of one pair of chunks, read from LDS a pair ahead of their use.
     constexpr int kPairs = 4, kProducts = FN * FM, kReads = FN + FM;
@@ -362,8 +401,8 @@ template <class C, class E>
 __global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
     using T = typename C::T;
     static_assert(C::BM == 256 && C::BN == 256 && C::WM == 128 && C::WN == 128 && C::DIRECT, "the large tile");
-    using LX = Lies<T, 128, C::XK>;
-    using LW = Lies<T, 128, C::WK>;
+    using LX = Lies<T, 128, C::XK, C::kB == 16>;
+    using LW = Lies<T, 128, C::WK, C::kB == 16>;
     constexpr int kElems = C::kElems, kStep = C::kStep, kQuarter = 128 * 128, kLoads = 16;
     enum { A0, B0, B1, A1 };  // in the order of their loads
     __shared__ __attribute__((aligned(1024))) char lds[2][4 * kQuarter];
@@ -371,8 +410,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
     const int M = g.live_m ? __builtin_amdgcn_readfirstlane(*g.live_m) : g.M;
     const int K = g.live_k ? __builtin_amdgcn_readfirstlane(*g.live_k) : g.K;
     const unsigned tiles_m = (M + 255) / 256, tiles_n = (g.N + C::kColsN - 1) / C::kColsN, tiles = tiles_m * tiles_n;
-    if (blockIdx.x >= tiles * (unsigned)(g.splits * g.products)) return;
-    const int turn = blockIdx.x / tiles, split = turn % g.splits, product = turn / g.splits;
+    const int splits = splits_in_use(g.splits, g.more, tiles);
+    if (blockIdx.x >= tiles * (unsigned)(splits * g.products)) return;
+    const int turn = blockIdx.x / tiles, split = turn % splits, product = turn / splits;
     int tm, tn;
     tile_of(blockIdx.x % tiles, tiles, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * 256, n0 = tn * C::kColsN;
@@ -380,7 +420,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
     // the order of the sum's steps, as in k_product
     const int whole1 = K / kStep, whole = whole1 + g.K2 / kStep;
     const int rest1 = K % kStep != 0, steps = whole + rest1 + (g.K2 % kStep != 0);
-    const int per = (steps + g.splits - 1) / g.splits, begin = split * per, end = min(steps, begin + per);
+    const int per = (steps + splits - 1) / splits, begin = split * per, end = min(steps, begin + per);
     auto second = [&](int s) { return s < whole ? s >= whole1 : s >= whole + rest1; };
     auto k_of = [&](int s) {
         if (s < whole) return (s < whole1 ? s : s - whole1) * kStep;
@@ -442,36 +482,53 @@ __global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
     };
 
     const Part part{m0 + w / 2 * 128, n0 + w % 2 * C::kWaveN, M, g.N, lane, w, tm, tn, split, product, &lds[0][0]};
-    f32x16 acc[4][4] = {};
+    typename C::Acc acc[C::FN][C::FM] = {};
     e.template start<C>(part, acc);
-    // A quarter's operands: two blocks, four pairs of chunks.  b2: the next B0,
-    // read while b0 is still in use.
+    // A quarter's operands: kHalf blocks, of each the parts of a stage's k.  b2:
+    // the next B0, read while b0 is still in use.
+    constexpr int kHalf = C::FM / 2, kParts = 8 / kHalf, kProducts = kHalf * kHalf * kParts;
     u32x4 a0[8], a1[8], b0[8], b1[8], b2[8];
     auto read = [&](int slot, int q, int i, u32x4 (&o)[8]) {
         const char* at = &lds[slot][q * kQuarter];
-        if (q == A0 || q == A1)
-            o[i] = operand<T, 128, C::XK>(at, i / 2, w / 2 * 64 + i % 2 * 32, lane);
+        const bool x = q == A0 || q == A1;
+        const int r0 = (x ? w / 2 : w % 2) * 64 + i % kHalf * C::kB;
+        if constexpr (C::kB == 16)
+            o[i] = x ? operand16<128, C::XK>(at, i / kHalf, r0, lane) : operand16<128, C::WK>(at, i / kHalf, r0, lane);
         else
-            o[i] = operand<T, 128, C::WK>(at, i / 2, w % 2 * 64 + i % 2 * 32, lane);
+            o[i] = x ? operand<T, 128, C::XK>(at, i / kHalf, r0, lane) : operand<T, 128, C::WK>(at, i / kHalf, r0, lane);
     };
-    // A quadrant's sixteen products, `between` called before each.
+    // A quadrant's products, each with an operand of the one before; `between` is
+    // called before every sixteenth of them.
     auto quadrant = [&](auto i0, auto j0, const u32x4 (&wq)[8], const u32x4 (&xq)[8], auto&& between) {
-        each(std::make_integer_sequence<int, 16>(), [&](auto u) {
-            between(u);
-            constexpr int p = u / 4, i = u / 2 % 2, j = u % 2;
-            acc[i0 + i][j0 + j] = mfma32(T(), wq[p * 2 + i], xq[p * 2 + j], acc[i0 + i][j0 + j]);
+        each(std::make_integer_sequence<int, kProducts>(), [&](auto u) {
+            constexpr int p = u / (kHalf * kHalf), i = i0 * kHalf + u / kHalf % kHalf, j = j0 * kHalf + (u / kHalf % 2 ? kHalf - 1 - u % kHalf : u % kHalf), each16 = kProducts / 16;
+            if constexpr (u % each16 == 0) between(std::integral_constant<int, u / each16>());
+            const u32x4 &a = wq[p * kHalf + i % kHalf], &b = xq[p * kHalf + j % kHalf];
+            if constexpr (C::kB == 16)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc[i][j], 0, 0, 0);
+            else
+                acc[i][j] = mfma32(T(), a, b, acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
         });
     };
     using Zero = std::integral_constant<int, 0>;
-    using Two = std::integral_constant<int, 2>;
+    using One = std::integral_constant<int, 1>;
     auto arrived = [&](auto left) {  // all but the last `left` loads, in every wave; and every wave has read what it asked for
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" :: "n"((int)left) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
     };
+    // The sums stay where they are, whatever comes before or after would rather
+    // have: else the compiler moves some of them about in the loop.
+    auto pin = [&] {
+        each(std::make_integer_sequence<int, C::FN * C::FM>(), [&](auto i) {
+            auto& v = acc[i / C::FM][i % C::FM];
+            asm volatile("" : "+a"(v));
+        });
+    };
     int s = begin;
     if (s < stop) {
+        pin();
         each(std::make_integer_sequence<int, kLoads>(), [&](auto i) { load(0, i, buffers(s)); });
         each(std::make_integer_sequence<int, kLoads>(), [&](auto i) { load(1, i, buffers(s + 1)); });
         arrived(std::integral_constant<int, 24>());
@@ -488,23 +545,25 @@ __global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
                 if constexpr (u % 2 == 1) b0[u / 2] = b2[u / 2];
                 if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, u / 4>(), f);
             });
-            quadrant(Two(), Zero(), b1, a0, [&](auto u) {
+            quadrant(One(), Zero(), b1, a0, [&](auto u) {
                 if constexpr (u < 8) read(slot, A1, u, a1);
                 if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, 4 + u / 4>(), f);
             });
             arrived(Left());
             const int other = 1 - slot;
-            quadrant(Two(), Two(), b1, a1, [&](auto u) {
+            quadrant(One(), One(), b1, a1, [&](auto u) {
                 if constexpr (u % 2 == 0) read(other, A0, u / 2, a0);
                 if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, 8 + u / 4>(), f);
             });
-            quadrant(Zero(), Two(), b0, a1, [&](auto u) {
+            quadrant(Zero(), One(), b0, a1, [&](auto u) {
                 if constexpr (u < 8) read(other, B0, u, b2);
                 if constexpr (u % 4 == 1) load(slot, std::integral_constant<int, 12 + u / 4>(), f);
             });
             slot = other;
         } while (++s < stop);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // and the last products' results are there
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
+        pin();
     }
     // what is no whole step, through registers, zero past the sum's end
     for (; s < end; ++s) {
@@ -530,9 +589,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) read(0, A0, i, a0), read(0, B0, i, b0), read(0, B1, i, b1), read(0, A1, i, a1);
         quadrant(Zero(), Zero(), b0, a0, [](auto) {});
-        quadrant(Two(), Zero(), b1, a0, [](auto) {});
-        quadrant(Two(), Two(), b1, a1, [](auto) {});
-        quadrant(Zero(), Two(), b0, a1, [](auto) {});
+        quadrant(One(), Zero(), b1, a0, [](auto) {});
+        quadrant(One(), One(), b1, a1, [](auto) {});
+        quadrant(Zero(), One(), b0, a1, [](auto) {});
     }
     __syncthreads();
     e.template finish<C>(part, acc);
@@ -541,7 +600,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_wide(Product g, E e) {
 // ------------------------------------------------------------- plain epilogue
 struct FromZero {
     template <class C>
-    __device__ void start(const Part&, f32x16 (&)[C::FN][C::FM]) const {}
+    __device__ void start(const Part&, typename C::Acc (&)[C::FN][C::FM]) const {}
 };
 // The sums as they are: rounded to O, or added to (ADD) or set as fp32 parts
 // [split][M][ld].
@@ -552,7 +611,7 @@ struct Store : FromZero {
     int64_t splits;  // from split to split
     bool add, whole;  // whole: four at once
     template <class C>
-    __device__ __attribute__((always_inline)) void finish(const Part& p, f32x16 (&acc)[C::FN][C::FM]) const {
+    __device__ __attribute__((always_inline)) void finish(const Part& p, typename C::Acc (&acc)[C::FN][C::FM]) const {
         static_assert(!C::PAIR, "one matrix");
         constexpr int kLanes = C::WN / 4, kAtOnce = 64 / kLanes, kPitch = C::WN + 4;
         const int c = p.lane % kLanes * 4, n = p.n0 + c;
@@ -585,15 +644,34 @@ inline bool fours(const void* p, int64_t ld, size_t elem_bytes) { return ld % 4 
 
 // Adds the splits' sums [splits][rows][N] in their order and rounds them.  row:
 // where each row of the result stands among the summed ones, -1 for a row of
-// zeros; null: in place.  Four columns a thread.
+// zeros; null: in place.  live: the rows that were in use, in tiles of `tile`.
+// Four columns a thread.
+struct Live {
+    const int* count;
+    int tile, more;
+};
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_join(const float* part, int splits, int64_t stride, const int* row, int M, int N, T* out) {
+__global__ __launch_bounds__(kThreads) void k_join(const float* part, int splits, int64_t stride, const int* row, Live live, int M, int N, T* out, bool whole) {
+    if (live.count) splits = splits_in_use(splits, live.more, (unsigned)((*live.count + live.tile - 1) / live.tile) * (unsigned)((N + live.tile - 1) / live.tile));
     const int across = (N + 3) / 4;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int m = (int)(i / across), n = (int)(i % across) * 4;
     if (m >= M) return;
     const int from = row ? row[m] : m;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
+    T* to = out + (int64_t)m * N + n;
+    if (whole) {
+        if (from >= 0)
+#pragma unroll 8
+            for (int s = 0; s < splits; ++s) {
+                float p[4];
+                get4(part + s * stride + (int64_t)from * N + n, p);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] += p[j];
+            }
+        put4(to, v);
+        return;
+    }
     if (from >= 0)
         for (int s = 0; s < splits; ++s) {
             const float* p = part + s * stride + (int64_t)from * N + n;
@@ -601,38 +679,54 @@ __global__ __launch_bounds__(kThreads) void k_join(const float* part, int splits
                 if (n + j < N) v[j] += p[j];
         }
     for (int j = 0; j < 4; ++j)
-        if (n + j < N) put(out + (int64_t)m * N + n + j, v[j]);
+        if (n + j < N) put(to + j, v[j]);
 }
 
 // ---------------------------------------------------------------- host side
 inline unsigned four_blocks(long long M, long long N) { return (unsigned)((M * ((N + 3) / 4) + kThreads - 1) / kThreads); }
 
-// The tile: the largest that still gives kEnough workgroups and does not compute
-// more than a quarter more past the edges.  Where tiles of 64 leave compute
-// units idle, the sum over k is split.
-constexpr int kEnough = 200, kSplitGroups = 512, kMaxSplits = 16;
-enum Size { kTile256, kTile128, kTile64 };
-inline long long tiles_at(long long M, long long N, int b) { return ((M + b - 1) / b) * ((N + b - 1) / b); }
-inline Size size_of(long long M, long long N, int products) {
-    auto fits = [&](int b) {
-        return tiles_at(M, N, b) * products >= kEnough && tiles_at(M, N, b) * 16 <= tiles_at(M, N, b / 2) * 5;
-    };
-    return fits(256) ? kTile256 : fits(128) ? kTile128 : kTile64;
-}
+// The tile of a product and the splits of its sum over k: those of the least time
+// by a plain count, of rounds of workgroups, steps in each, and the bytes of the
+// splits' sums.  Microseconds: a tile's step (128 bytes of k; two tiles of 64 share
+// a compute unit), and what a workgroup takes beside its steps.  kTile192 is 192
+// rows by 128 columns, for products of up to that many rows, which it reads W
+// once for; only where `tall`.
+constexpr int kMaxSplits = 32;
+enum Size { kTile256, kTile128, kTile64, kTile192 };
+struct Plan {
+    Size size;
+    int splits;
+};
 inline long long step_of(spec_dtype d) { return 128 / (long long)elem(d); }
-inline int splits_at(spec_dtype d, long long M, long long N, long long K, int products) {
-    if (size_of(M, N, products) != kTile64) return 1;
-    const long long steps = (K + step_of(d) - 1) / step_of(d), want = kSplitGroups / (tiles_at(M, N, 64) * products);
-    long long s = want < steps / 4 ? want : steps / 4;
-    s = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
-    const long long per = (steps + s - 1) / s;
-    return (int)((steps + per - 1) / per);  // no split without steps
+inline Plan plan_of(spec_dtype d, long long M, long long N, long long K, int products, bool splitting, bool tall) {
+    static const double kStepTime[2][4] = {{7.2, 1.85, 0.95, 2.8}, {1.4, 0.6, 0.5, 0.5}}, kBeside[4] = {12, 7, 5, 7};
+    static const int kRows[4] = {256, 128, 64, 192}, kColumns[4] = {256, 128, 64, 128};
+    const long long steps = (K + step_of(d) - 1) / step_of(d);
+    Plan best{kTile64, 1};
+    double least = 1e30;
+    for (int z = 0; z < (tall ? 4 : 3); ++z) {
+        const long long slots = z == kTile64 ? 512 : 256;
+        const long long tiles = ((M + kRows[z] - 1) / kRows[z]) * ((N + kColumns[z] - 1) / kColumns[z]) * products;
+        for (int s = 1; s <= (splitting ? kMaxSplits : 1) && s <= steps; ++s) {
+            const long long per = (steps + s - 1) / s, rounds = (tiles * s + slots - 1) / slots;
+            double us = rounds * (per * kStepTime[d == SPEC_BF16][z] + kBeside[z]);
+            if (s > 1) us += 4 + (double)(s * M * N * products) * 8 / 4e6;
+            if (us < least) least = us, best = {(Size)z, (int)((steps + per - 1) / per)};
+        }
+    }
+    return best;
+}
+
+template <typename T>
+void join(const float* part, int splits, const int* row, Live live, int M, int N, T* out, hipStream_t st) {
+    const bool whole = fours(part, N, 4) && fours(out, N, sizeof(T));
+    k_join<T><<<four_blocks(M, N), kThreads, 0, st>>>(part, splits, (int64_t)M * N, row, live, M, N, out, whole);
 }
 
 template <class C, class E>
 void launch_tile(const Product& g, const E& e, hipStream_t st) {
     const unsigned grid = (unsigned)((g.M + C::BM - 1) / C::BM) * (unsigned)((g.N + C::kColsN - 1) / C::kColsN) *
-                          (unsigned)(g.splits * g.products);
+                          (unsigned)((g.more > g.splits ? g.more : g.splits) * g.products);
     if constexpr (C::BM == 256)
         k_wide<C, E><<<grid, kThreads, 0, st>>>(g, e);
     else
@@ -642,7 +736,7 @@ inline bool aligned(const Product& g, size_t e) {
     uintptr_t a = (uintptr_t)g.x[0] | (uintptr_t)g.w[0] | (uintptr_t)g.x[1] | (uintptr_t)g.w[1];
     return a % 16 == 0 && g.ldx * e % 16 == 0 && g.ldw * e % 16 == 0;
 }
-// g.splits stands for a tile of 64, like `size`, whatever the alignment.
+// What is not aligned takes tiles of 64 through registers, with the same splits.
 template <typename T, bool XK, bool WK, class E>
 void launch_product(const Product& g, const E& e, Size size, hipStream_t st) {
     if (!aligned(g, sizeof(T)))
