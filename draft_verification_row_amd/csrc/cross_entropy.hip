@@ -163,9 +163,22 @@ struct Stats : Logits<T> {
     }
 };
 
+// The outputs of row r from its maximum, sum and token's logit.  stats: the
+// maximum and 1 / S, both 0 for a row of -inf alone.
+__device__ inline void finish_row(const Outputs& o, int64_t r, int x, int V, MaxSum v, float picked) {
+    if (!in_use(o, r, x, V)) return;
+    const bool some = v.top != -INFINITY || v.sum != v.sum;
+    const float ls = logf(v.sum);
+    o.loss[r] = some ? ls - (picked - v.top) : INFINITY;
+    o.lse[r] = some ? v.top + ls : -INFINITY;
+    if (o.stats) {
+        o.stats[2 * r] = some ? v.top : 0.f;
+        o.stats[2 * r + 1] = some ? 1.f / v.sum : 0.f;
+    }
+}
+
 // Folds the tiles' parts of each row in use and writes the outputs of its row:
-// `across` rows a workgroup, the parts of each over the other threads.  stats:
-// the row's maximum and 1 / S, both 0 for a row of -inf alone.
+// `across` rows a workgroup, the parts of each over the other threads.
 struct Fold {
     const MaxSum* part;
     const float* picked;
@@ -189,28 +202,92 @@ __global__ __launch_bounds__(kLiveThreads) void k_fold(Fold a) {
         __syncthreads();
     }
     if (g != 0 || m >= rows) return;
-    v = red[t];
     const int64_t r = a.live ? a.live[m] : m;
-    const Outputs& o = a.out;
-    if (!in_use(o, r, a.tokens[r], a.V)) return;
-    const bool some = v.top != -INFINITY || v.sum != v.sum;
-    const float ls = logf(v.sum);
-    o.loss[r] = some ? ls - (a.picked[m] - v.top) : INFINITY;
-    o.lse[r] = some ? v.top + ls : -INFINITY;
-    if (o.stats) {
-        o.stats[2 * r] = some ? v.top : 0.f;
-        o.stats[2 * r + 1] = some ? 1.f / v.sum : 0.f;
+    finish_row(a.out, r, a.tokens[r], a.V, red[t], a.picked[m]);
+}
+
+// Where the product's sum over k is split, because its tiles are few, the splits'
+// sums of the logits are in memory, part [split][M][V] (a few million in all).
+struct Small {
+    const float* part;
+    int splits, M, V;
+    const void* bias;
+    const int32_t* tokens;
+    const int *live, *count;  // or null: every row
+};
+template <typename T>
+__device__ inline float logit(const Small& a, int m, int v) {
+    float z = a.bias ? to_f(static_cast<const T*>(a.bias)[v]) : 0.f;
+    for (int s = 0; s < a.splits; ++s) z += a.part[((int64_t)s * a.M + m) * a.V + v];
+    return z;
+}
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_small_stats(Small a, Outputs out) {
+    __shared__ MaxSum red[kThreads];
+    __shared__ float picked;
+    const int m = blockIdx.x, t = threadIdx.x;
+    if (a.live && m >= *a.count) return;
+    const int64_t r = a.live ? a.live[m] : m;
+    const int x = a.tokens[r];
+    MaxSum all = {-INFINITY, 0.f};
+    for (int v = t; v < a.V; v += kThreads) {
+        const float z = logit<T>(a, m, v);
+        all = joined(all, {z, z == -INFINITY ? 0.f : z == z ? 1.f : z});
+        if (v == x) picked = z;
     }
+    red[t] = all;
+    __syncthreads();
+    for (int s = kThreads / 2; s > 0; s /= 2) {
+        if (t < s) red[t] = joined(red[t], red[t + s]);
+        __syncthreads();
+    }
+    if (t == 0) finish_row(out, r, x, a.V, red[0], picked);
 }
 
 // ------------------------------------------------------------------ backward
+// What dz of a row needs: dz = both p - one [token].
+struct Weights {
+    const float *stats, *g_loss, *g_lse;  // a gradient may be null
+};
+struct RowWeights {
+    float top, inv, one, both;
+    __device__ float of(float z) const {
+        // p from the difference itself; 0 whatever the weight where p = 0
+        const float q = exp_of(z - top) * inv;
+        return q == 0.f ? 0.f : both * q;
+    }
+};
+__device__ inline RowWeights weights_of(const Weights& a, int64_t r) {
+    RowWeights w{a.stats[2 * r], a.stats[2 * r + 1], 0.f, 0.f};
+    w.one = a.g_loss && w.inv != 0.f ? a.g_loss[r] : 0.f;
+    w.both = w.one + (a.g_lse ? a.g_lse[r] : 0.f);
+    return w;
+}
+
+// From the logits in memory; dz unrounded takes the first split's place.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_small_slope(Small a, Weights weights, T* dz, int64_t ld) {
+    const int m = blockIdx.x;
+    if (m >= *a.count) return;
+    const int64_t r = a.live[m];
+    const int x = a.tokens[r];
+    const RowWeights w = weights_of(weights, r);
+    float* first = const_cast<float*>(a.part) + (int64_t)m * a.V;
+    for (int v = threadIdx.x; v < a.V; v += kThreads) {
+        float d = w.of(logit<T>(a, m, v));
+        if (v == x) d -= w.one;
+        first[v] = d;
+        put(dz + m * ld + v, d);
+    }
+}
+
 // Turns a piece's logits, columns v0 on, into dz, rounded, dz [rows][ld]; and
 // its columns' sums over each wave's rows, unrounded, part [tile and wave][V].
 template <typename T>
 struct Slope : Logits<T> {  // the bias: of the piece
     const int32_t* tokens;
     const int* live;
-    const float *stats, *g_loss, *g_lse;  // a gradient may be null
+    Weights weights;
     int v0, V;
     T* dz;
     int64_t ld;
@@ -228,21 +305,15 @@ struct Slope : Logits<T> {  // the bias: of the piece
             float minus[kBlocks];
             each(std::make_integer_sequence<int, kBlocks>(), [&](auto k) __attribute__((always_inline)) {
                 const int m = p.m0 + j * 32 + k * C::kB + l;
-                float top = 0.f, inv = 0.f, one = 0.f, both = 0.f;
+                RowWeights row{0.f, 0.f, 0.f, 0.f};
                 at[k] = -1;
                 if (m < p.M) {
                     const int r = live[m];
-                    top = stats[2 * (int64_t)r], inv = stats[2 * (int64_t)r + 1];
-                    one = g_loss && inv != 0.f ? g_loss[r] : 0.f;
-                    both = one + (g_lse ? g_lse[r] : 0.f);
+                    row = weights_of(weights, r);
                     at[k] = tokens[r] - v0 - p.n0;
                 }
-                minus[k] = one;
-                values<C>(acc, std::integral_constant<int, j * kBlocks + k>(), [&](float z) __attribute__((always_inline)) {
-                    // p from the difference itself; 0 whatever the weight where p = 0
-                    const float q = exp_of(z - top) * inv;
-                    return q == 0.f ? 0.f : both * q;
-                });
+                minus[k] = row.one;
+                values<C>(acc, std::integral_constant<int, j * kBlocks + k>(), [&](float z) __attribute__((always_inline)) { return row.of(z); });
             });
             lay<C>(p, acc, j);
             float* rows = rows_of<C>(p);
@@ -293,7 +364,7 @@ __global__ __launch_bounds__(kLiveThreads) void k_bias_fold(const float* part, c
 }
 
 // ---------------------------------------------------------------- host side
-inline bool entropy_ok(spec_dtype d, long long M, long long V, long long K) {
+inline bool entropy_ok(const spec_dtype& d, long long M, long long V, long long K) {
     const int t = value_of(d);
     return (t == SPEC_BF16 || t == SPEC_F32) && M >= 1 && V >= 1 && K >= 1 && M <= SPEC_MAX_LINEAR && V <= SPEC_MAX_LINEAR &&
            K <= SPEC_MAX_LINEAR && M * K < (1ll << 33) && V * K < (1ll << 33);
@@ -339,7 +410,12 @@ void pack(const void* x, const int* live, const int* count, long long rows, int 
 }
 inline size_t matrix_bytes(spec_dtype d, long long rows, long long ld) { return align_up((size_t)(rows * ld) * elem(d), 256); }
 
+// Few tiles of a long sum: it is split.
+inline Plan small_plan(spec_dtype d, long long M, long long V, long long K) { return plan_of(d, M, V, K, 1, true, false); }
+inline size_t small_bytes(const Plan& p, long long M, long long V) { return p.splits > 1 ? align_up((size_t)(p.splits * M * V) * 4, 256) : 0; }
+
 struct ForwardLayout {
+    Plan small;
     size_t live, place, count, x, w, part, picked, total;
     bool few, packs;
 };
@@ -347,13 +423,14 @@ inline ForwardLayout forward_layout(spec_dtype d, long long M, long long V, long
     ForwardLayout l;
     l.few = M <= 64;
     l.packs = packs_weight(d, M, K);
+    l.small = small_plan(d, M, V, K);
     l.live = 0;
     l.place = align_up(l.live + (l.few ? 0 : M * 4), 256);
     l.count = align_up(l.place + (l.few ? 0 : M * 4), 256);
     l.x = l.count + 256;
     l.w = l.x + (l.few ? 0 : matrix_bytes(d, M, padded(d, K)));
     l.part = l.w + (l.packs ? matrix_bytes(d, V, padded(d, K)) : 0);
-    l.picked = align_up(l.part + (size_t)((V + 63) / 64 * M) * sizeof(MaxSum), 256);
+    l.picked = align_up(l.part + (l.small.splits > 1 ? small_bytes(l.small, M, V) : (size_t)((V + 63) / 64 * M) * sizeof(MaxSum)), 256);
     l.total = align_up(l.picked + M * 4, 256);
     return l;
 }
@@ -383,6 +460,13 @@ void entropy_forward(const void* x, const void* weight, const void* bias, const 
             g.K = (int)ld;  // the padding is zero
         }
     }
+    if (lay.small.splits > 1) {
+        float* z = reinterpret_cast<float*>(ws + lay.part);
+        g.splits = lay.small.splits;
+        launch_product<T, false, false>(g, Store<float>{{}, {z, z}, V, (int64_t)M * V, false, fours(z, V, 4)}, lay.small.size, st);
+        k_small_stats<T><<<M, kThreads, 0, st>>>({z, g.splits, M, V, bias, tokens, live, count}, out);
+        return;
+    }
     const Shape s = shape_of(d, M, V, K);
     launch_logits<T>(g, Stats<T>{{static_cast<const T*>(bias)}, tokens, live, M, part, picked}, s, st);
     const int bn = tiling(s, aligned(g, sizeof(T))).bn;
@@ -400,12 +484,14 @@ inline int piece_of(spec_dtype d, long long M, long long V) {
 struct BackwardLayout {
     size_t live, place, count, x, w, dz, dx, dw, part, total;
     int piece, more;  // more: splits of dx where few rows are in use
-    Plan px, pw;
+    Plan px, pw, small;
     bool packs;
 };
 inline BackwardLayout backward_layout(spec_dtype d, long long M, long long V, long long K) {
     BackwardLayout l;
     l.piece = piece_of(d, M, V);
+    l.small = small_plan(d, M, V, K);
+    if (l.small.splits > 1) l.piece = (int)V;
     l.packs = packs_weight(d, M, K);
     l.px = plan_of(d, M, K, l.piece, 1, true, false);
     l.pw = plan_of(d, l.piece, K, M, 1, true, false);
@@ -421,7 +507,7 @@ inline BackwardLayout backward_layout(spec_dtype d, long long M, long long V, lo
     l.dx = l.dz + matrix_bytes(d, M, padded(d, l.piece));
     l.dw = align_up(l.dx + (size_t)(l.more * M * K) * 4, 256);
     l.part = align_up(l.dw + (l.pw.splits > 1 ? (size_t)l.pw.splits * l.piece * K * 4 : 0), 256);
-    l.total = align_up(l.part + (size_t)((M + 31) / 32 * V) * 4, 256);
+    l.total = align_up(l.part + (l.small.splits > 1 ? small_bytes(l.small, M, V) : (size_t)((M + 31) / 32 * V) * 4), 256);
     return l;
 }
 
@@ -455,8 +541,17 @@ void entropy_backward(const void* x, const void* weight, const void* bias, const
         const int n = V - v0 < lay.piece ? V - v0 : lay.piece;
         const T* w = wp + v0 * ldw;
         const Product z{{xp, xp}, {w, w}, ld, ldw, M, n, kz, 0, count, nullptr, 1, 1, 0};
-        tiles = tiling(shape, aligned(z, sizeof(T)));
-        launch_logits<T>(z, Slope<T>{{bias ? static_cast<const T*>(bias) + v0 : nullptr}, tokens, live, stats, g_loss, g_lse, v0, V, dz, ldz, part}, shape, st);
+        if (lay.small.splits > 1) {
+            float* logits = reinterpret_cast<float*>(ws + lay.part);
+            Product split = z;
+            split.splits = lay.small.splits;
+            launch_product<T, false, false>(split, Store<float>{{}, {logits, logits}, V, (int64_t)M * V, false, fours(logits, V, 4)}, lay.small.size, st);
+            k_small_slope<T><<<M, kThreads, 0, st>>>({logits, split.splits, M, V, bias, tokens, live, count}, {stats, g_loss, g_lse}, dz, ldz);
+            tiles = {1, 1, 1};  // the bias gradient sums rows
+        } else {
+            tiles = tiling(shape, aligned(z, sizeof(T)));
+            launch_logits<T>(z, Slope<T>{{bias ? static_cast<const T*>(bias) + v0 : nullptr}, tokens, live, {stats, g_loss, g_lse}, v0, V, dz, ldz, part}, shape, st);
+        }
         if (gx) {
             const Product p{{dz, dz}, {w, w}, ldz, ldw, M, K, n, 0, count, nullptr, 1, lay.px.splits, lay.more};
             dx_tile = aligned(p, sizeof(T)) ? 256 >> lay.px.size : 64;

@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kThreads) void k_table_grad(TableGrad a) {
 
 // ---------------------------------------------------------------- host side
 constexpr long long kMaxTable = 1ll << 34;  // elements: launches stay below 2^32 threads
-inline bool embedding_ok(spec_dtype d, long long n, long long V, long long H) {
+inline bool embedding_ok(const spec_dtype& d, long long n, long long V, long long H) {
     const int t = value_of(d);
     return (t == SPEC_BF16 || t == SPEC_F32) && n >= 1 && V >= 1 && H >= 1 && n <= SPEC_MAX_LINEAR && V <= SPEC_MAX_LINEAR &&
            H <= SPEC_MAX_LINEAR && n * H < kMaxTable && V * H < kMaxTable;

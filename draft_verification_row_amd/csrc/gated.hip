@@ -124,7 +124,33 @@ __global__ __launch_bounds__(kThreads) void k_gated_few(Product g, Gate<T> e) {
     }
 }
 
-// The splits' sums of g and u, [splits][2][M][N], added and finished.
+// The sums of a split of k as they are, part [splits][2][M][N]: g, then u.
+struct GateSums : FromZero {
+    float* part;
+    bool whole;
+    template <class C>
+    __device__ __attribute__((always_inline)) void finish(const Part& p, typename C::Acc (&acc)[C::FN][C::FM]) const {
+        constexpr int kLanes = C::kWaveN / 4, kAtOnce = 64 / kLanes, kPitch = C::WN + 4;
+        const int c = p.lane % kLanes * 4, n = p.n0 + c;
+        turned<C>(p, acc, [&](int j, float* rows) __attribute__((always_inline)) {
+            if (n >= p.N) return;
+            for (int r = p.lane / kLanes; r < 32; r += kAtOnce) {
+                const int m = p.m0 + j * 32 + r;
+                if (m >= p.M) break;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const f32x4 v = *reinterpret_cast<const f32x4*>(rows + r * kPitch + k * C::kWaveN + c);
+                    float* to = part + ((int64_t)(p.split * 2 + k) * p.M + m) * p.N + n;
+                    if (whole)
+                        *reinterpret_cast<f32x4*>(to) = v;
+                    else
+                        for (int i = 0; i < 4 && n + i < p.N; ++i) to[i] = v[i];
+                }
+            }
+        });
+    }
+};
+// They are added and finished.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_gated_join(const float* part, int splits, int M, int N, Gate<T> e) {
     const int across = (N + 3) / 4;
@@ -176,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void k_gated_slopes(GateSlope a) {
 }
 
 // ---------------------------------------------------------------- host side
-inline bool gated_ok(spec_dtype d, long long M, long long N, long long K) {
+inline bool gated_ok(const spec_dtype& d, long long M, long long N, long long K) {
     const int t = value_of(d);
     return (t == SPEC_BF16 || t == SPEC_F32) && M >= 1 && N >= 1 && K >= 1 && M <= SPEC_MAX_LINEAR && N <= SPEC_MAX_LINEAR &&
            K <= SPEC_MAX_LINEAR && M * N < (1ll << 33) && M * K < (1ll << 33) && N * K < (1ll << 33);
@@ -222,23 +248,16 @@ Padded pad_rows(const void* x, const void* gate, const void* up, spec_dtype d, i
     return {px, pg, pu, ld};
 }
 
-template <typename T>
-void gated_forward(Product g, const Gate<T>& e, spec_dtype d, char* ws, hipStream_t st) {
-    if (g.M <= 16) {
-        const unsigned grid = (unsigned)((g.N + 15) / 16);
-        if (aligned(g, sizeof(T)))
-            k_gated_few<T, true><<<grid, kThreads, 0, st>>>(g, e);
-        else
-            k_gated_few<T, false><<<grid, kThreads, 0, st>>>(g, e);
-        return;
-    }
-    if (packs_pair(d, g.M, g.K)) {
-        const Padded p = pad_rows<T>(g.x[0], g.w[0], g.w[1], d, g.M, g.N, g.K, ws, st);
-        g.x[0] = g.x[1] = p.x, g.w[0] = p.gate, g.w[1] = p.up;
-        g.ldx = g.ldw = p.ld;
-        g.K = (int)p.ld;  // the padding is zero
-    }
-    const Size size = plan_of(d, g.M, 2ll * g.N, g.K, 1, false, true).size;
+inline Plan gated_plan(spec_dtype d, long long M, long long N, long long K) { return plan_of(d, M, 2 * N, K, 1, true, true); }
+inline size_t gated_packs(spec_dtype d, long long M, long long N, long long K) {
+    return packs_pair(d, M, K) ? packed_bytes(d, M, K) + 2 * packed_bytes(d, N, K) : 0;
+}
+inline size_t gated_bytes(spec_dtype d, long long M, long long N, long long K) {
+    const int s = M > 16 ? gated_plan(d, M, N, K).splits : 1;
+    return gated_packs(d, M, N, K) + (s > 1 ? align_up((size_t)(2 * s * M * N) * 4, 256) : 0) + 256;
+}
+template <typename T, class E>
+void launch_pair(const Product& g, const E& e, Size size, hipStream_t st) {
     if (!aligned(g, sizeof(T)))
         launch_tile<Tile<T, 64, 128, 32, 64, 2, false, false, true, false>>(g, e, st);
     else if (size == kTile256)
@@ -249,6 +268,34 @@ void gated_forward(Product g, const Gate<T>& e, spec_dtype d, char* ws, hipStrea
         launch_tile<Tile<T, 128, 128, 64, 64, 4, false, false, true, true>>(g, e, st);
     else
         launch_tile<Tile<T, 64, 128, 32, 64, 3, false, false, true, true>>(g, e, st);
+}
+
+template <typename T>
+void gated_forward(Product g, const Gate<T>& e, spec_dtype d, char* ws, hipStream_t st) {
+    if (g.M <= 16) {
+        const unsigned grid = (unsigned)((g.N + 15) / 16);
+        if (aligned(g, sizeof(T)))
+            k_gated_few<T, true><<<grid, kThreads, 0, st>>>(g, e);
+        else
+            k_gated_few<T, false><<<grid, kThreads, 0, st>>>(g, e);
+        return;
+    }
+    const int k = g.K;
+    const Plan plan = gated_plan(d, g.M, g.N, k);
+    if (packs_pair(d, g.M, g.K)) {
+        const Padded p = pad_rows<T>(g.x[0], g.w[0], g.w[1], d, g.M, g.N, g.K, ws, st);
+        g.x[0] = g.x[1] = p.x, g.w[0] = p.gate, g.w[1] = p.up;
+        g.ldx = g.ldw = p.ld;
+        g.K = (int)p.ld;  // the padding is zero
+    }
+    if (plan.splits == 1) {
+        launch_pair<T>(g, e, plan.size, st);
+        return;
+    }
+    float* part = reinterpret_cast<float*>(ws + gated_packs(d, g.M, g.N, k));
+    g.splits = plan.splits;
+    launch_pair<T>(g, GateSums{{}, part, fours(part, g.N, 4)}, plan.size, st);
+    k_gated_join<T><<<four_blocks(g.M, g.N), kThreads, 0, st>>>(part, plan.splits, g.M, g.N, e);
 }
 
 // The gradients' workspace: dg and du, and the sums of split products.
@@ -316,7 +363,7 @@ void gated_backward(const void* x, const void* gate, const void* up, const float
 
 extern "C" size_t spec_gated_linear_workspace_bytes(spec_dtype dtype, int M, int N, int K) {
     if (!gated_ok(dtype, M, N, K)) return 0;
-    return packs_pair(dtype, M, K) ? packed_bytes(dtype, M, K) + 2 * packed_bytes(dtype, N, K) : 256;
+    return gated_bytes(dtype, M, N, K);
 }
 
 extern "C" spec_status spec_gated_linear(const void* x, const void* gate, const void* up, spec_dtype dtype,

@@ -115,6 +115,14 @@ def test_entropy_larger(M, V, K, dtype):
     check(M, V, K, dtype, bias=M % 4 == 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,V,K", [(6, 100, 8000), (40, 1000, 5001), (100, 300, 4096), (300, 1501, 8192)])
+def test_entropy_few_tiles_split(M, V, K, dtype):
+    """Few logits of long sums: K over several workgroups."""
+    check(M, V, K, dtype, bias=True, masked=0.2)
+    check(M, V, K, dtype)
+
+
 @pytest.mark.parametrize("dtype,V", [("bf16", 50001), ("f32", 30000)])
 def test_entropy_in_pieces_of_the_vocabulary(dtype, V):
     """More than 512 MiB of dz: the second piece adds to x's gradient."""

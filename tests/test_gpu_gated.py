@@ -119,6 +119,13 @@ def test_gated_long_sums():
     check(3, 40000, 24, "bf16", "none")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(40, 100, 8000), (17, 65, 5001), (200, 300, 4096)])
+def test_gated_few_tiles_split(M, N, K, dtype):
+    """Few outputs of a long sum: K over several workgroups."""
+    check(M, N, K, dtype, "gelu")
+
+
 def test_gated_special_values():
     """NaN and infinities stay in their rows."""
     for M in (5, 40):
