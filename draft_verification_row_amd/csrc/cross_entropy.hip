@@ -118,7 +118,8 @@ struct Logits {
 
 // Leaves each row's maximum and sum over the tile's columns, part [tile][M],
 // and the row's token's logit.  A lane has the columns of one row, so that most
-// of it is done without a word to another lane.
+// of it is done without a word to another lane.  7373 x 128256 x 4096 bf16 5.7 to
+// 5.9 ms (1310 to 1360 TFLOP/s); 6 rows 155 us, W read at 6.8 TB/s.
 template <typename T>
 struct Stats : Logits<T> {
     const int32_t* tokens;

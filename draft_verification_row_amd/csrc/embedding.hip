@@ -92,7 +92,8 @@ __global__ __launch_bounds__(kThreads) void k_lookup(Lookup a) {
 // ------------------------------------------------------------------- sorting
 // The place of each position among all, by token and then by position: the
 // number of positions that come before it.  64 positions a workgroup, a lane
-// each, whose waves count over a share of the tokens each, read as scalars.
+// each, whose waves count over a share of the tokens each, read as scalars:
+// 28 us for 16384 positions, growing with their square.
 // Tokens outside the table are not below V as unsigned numbers: they come last.
 constexpr int kRankWaves = 16;
 __global__ __launch_bounds__(64 * kRankWaves) void k_rank(const uint32_t* __restrict__ tokens, int n, uint32_t* sorted, int* position) {
@@ -168,7 +169,9 @@ __global__ __launch_bounds__(kThreads) void k_starts(const uint32_t* sorted, int
 }
 
 // A workgroup writes kRowsEach rows of the table's gradient after each other, or
-// that many groups of narrower rows, `lanes` threads a row.
+// that many groups of narrower rows, `lanes` threads a row.  128256 x 4096 bf16,
+// 16384 tokens: 270 us (4.4 TB/s written and read), 215 with no token (4.9 TB/s;
+// 4 or 16 rows each are 4 to 8% slower, stores through the caches 5%).
 constexpr int kRowsEach = 8;
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_table_grad(TableGrad a) {
