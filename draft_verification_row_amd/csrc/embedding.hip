@@ -285,7 +285,7 @@ void table_grad(const int32_t* tokens, const void* dy, float scale, int n, int V
 extern "C" spec_status spec_embedding(const void* weight, spec_dtype dtype, const int32_t* tokens, float scale, int n, int V, int H,
                                       void* out, void* stream) {
     if (!type_ok(dtype)) return SPEC_EDTYPE;
-    if (!embedding_ok(dtype, n, V, H) || !weight || !tokens || !out) return SPEC_EINVAL;
+    if (!embedding_ok(dtype, n, V, H) || !isfinite(scale) || !weight || !tokens || !out) return SPEC_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (value_of(dtype) == SPEC_BF16)
         lookup<bf16>(weight, tokens, scale, n, V, H, out, st);
@@ -301,7 +301,7 @@ extern "C" size_t spec_embedding_grad_workspace_bytes(spec_dtype dtype, int n, i
 extern "C" spec_status spec_embedding_grad(const int32_t* tokens, const void* grad_out, spec_dtype dtype, float scale, int n, int V,
                                            int H, void* grad_weight, void* workspace, size_t workspace_bytes, void* stream) {
     if (!type_ok(dtype)) return SPEC_EDTYPE;
-    if (!embedding_ok(dtype, n, V, H) || !tokens || !grad_out || !grad_weight) return SPEC_EINVAL;
+    if (!embedding_ok(dtype, n, V, H) || !isfinite(scale) || !tokens || !grad_out || !grad_weight) return SPEC_EINVAL;
     if (!ws_ok(workspace, workspace_bytes, spec_embedding_grad_workspace_bytes(dtype, n, V, H))) return SPEC_EWORKSPACE;
     char* ws = static_cast<char*>(workspace);
     const hipStream_t st = static_cast<hipStream_t>(stream);

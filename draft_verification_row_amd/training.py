@@ -84,6 +84,8 @@ def spec_embedding(weight: torch.Tensor, tokens: torch.Tensor, *, scale: float =
     _check(tokens, "tokens", torch.int32)
     _same_device(W.device, tokens=tokens)
     scale = float(scale)
+    if not abs(scale) <= torch.finfo(torch.float32).max:
+        raise SpecVerifyError(f"scale must be finite in float32, got {scale}")
     if _wants_grad(W):
         y = _Embedding.apply(W, tokens, scale)
         _mark_leaves(y)

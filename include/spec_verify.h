@@ -609,7 +609,8 @@ spec_status spec_linear_grad(const void *x, const void *weight, const void *prea
  * of zeros, any other outside [0, V) a row of NaN.
  *
  *   weight (W) [V][H], out [n][H] dtype; tokens [n] int32
- * 1 <= n, V, H <= SPEC_MAX_LINEAR, and n * H and V * H below 2^34.
+ * scale is finite.  1 <= n, V, H <= SPEC_MAX_LINEAR, and n * H and V * H below
+ * 2^34.
  */
 spec_status spec_embedding(const void *weight, spec_dtype dtype, const int32_t *tokens,
                            float scale, int n, int V, int H, void *out, void *stream);

@@ -45,7 +45,8 @@ def test_embedding_argument_errors(lib):
 
     for c in (f, g):
         assert c(dt=2) == EDTYPE and c(dt=-1) == EDTYPE
-        for bad in (dict(tok=None), dict(n=0), dict(V=0), dict(H=0), dict(n=-3), dict(n=1 << 21), dict(V=1 << 20, H=1 << 15)):
+        for bad in (dict(tok=None), dict(n=0), dict(V=0), dict(H=0), dict(n=-3), dict(n=1 << 21), dict(V=1 << 20, H=1 << 15),
+                    dict(scale=float("inf")), dict(scale=float("nan"))):
             assert c(**bad) == EINVAL, bad
     assert f(w=None) == EINVAL and f(y=None) == EINVAL and g(gy=None) == EINVAL and g(gw=None) == EINVAL
     assert g(ws=None) == EWORKSPACE and g(ws=WS + 64) == EWORKSPACE and g(wsb=need - 1) == EWORKSPACE
@@ -118,6 +119,7 @@ def test_binding_refusals():
     bad = [
         lambda: sv.spec_embedding(W, tok.long()), lambda: sv.spec_embedding(W.half(), tok), lambda: sv.spec_embedding(W[0], tok),
         lambda: sv.spec_embedding(W.t(), tok), lambda: sv.spec_embedding(W[:0], tok), lambda: sv.spec_embedding(W, tok.t()),
+        lambda: sv.spec_embedding(W, tok, scale=float("nan")), lambda: sv.spec_embedding(W, tok, scale=1e39),
         lambda: sv.spec_embedding(W, tok.cpu()), lambda: sv.spec_embedding(W, [1, 2]),
         lambda: sv.spec_embedding(torch.zeros(1, (1 << 20) + 1, device="cuda"), tok),
         lambda: sv.spec_gated_linear(X, W, W.bfloat16()), lambda: sv.spec_gated_linear(X.half(), W.half(), W.half()),
