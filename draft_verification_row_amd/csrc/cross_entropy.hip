@@ -282,8 +282,16 @@ __global__ __launch_bounds__(kThreads) void k_small_slope(Small a, Weights weigh
     }
 }
 
+// A product's tiles, and the waves that share a tile's rows out.
+struct Tiling {
+    int bm, bn, waves_m;
+};
+// The waves' shares of `rows` rows: of whole tiles, since a wave of a tile
+// writes its sums whether or not it has a row.
+__host__ __device__ inline int wave_rows(int rows, const Tiling& t) { return (rows + t.bm - 1) / t.bm * t.waves_m; }
+
 // Turns a piece's logits, columns v0 on, into dz, rounded, dz [rows][ld]; and
-// its columns' sums over each wave's rows, unrounded, part [tile and wave][V].
+// its columns' sums over each wave's rows, unrounded, part [wave_rows][V].
 template <typename T>
 struct Slope : Logits<T> {  // the bias: of the piece
     const int32_t* tokens;
@@ -349,10 +357,10 @@ struct Slope : Logits<T> {  // the bias: of the piece
 // dbias[v] = the sum of the parts, in a fixed order: 64 columns a workgroup,
 // every sixteenth part to a wave.
 template <typename T>
-__global__ __launch_bounds__(kLiveThreads) void k_bias_fold(const float* part, const int* count, int tile, int waves, int V, T* out) {
+__global__ __launch_bounds__(kLiveThreads) void k_bias_fold(const float* part, const int* count, Tiling tiles, int V, T* out) {
     __shared__ float sums[kLiveThreads / 64][64];
     const int c = threadIdx.x & 63, w = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
-    const int parts = (*count + tile - 1) / tile * waves;
+    const int parts = wave_rows(*count, tiles);
     float s = 0.f;
     if (n < V)
         for (int i = w; i < parts; i += kLiveThreads / 64) s += part[(int64_t)i * V + n];
@@ -383,9 +391,6 @@ inline Shape shape_of(spec_dtype d, long long M, long long V, long long K) {
 // Where W's rows are no whole chunks, they are copied to padded ones first if
 // more than 64 rows use them.
 inline bool packs_weight(spec_dtype d, long long M, long long K) { return padded(d, K) != K && M > 64; }
-struct Tiling {
-    int bm, bn, waves_m;
-};
 inline Tiling tiling(Shape s, bool direct) {
     if (!direct || s == kLogits64) return {64, 64, 2};
     return s == kRows32 ? Tiling{32, 128, 1} : s == kRows64 ? Tiling{64, 128, 1} : s == kRows192 ? Tiling{192, 128, 2} : s == kLogits256 ? Tiling{256, 256, 2} : Tiling{128, 128, 2};
@@ -508,7 +513,10 @@ inline BackwardLayout backward_layout(spec_dtype d, long long M, long long V, lo
     l.dx = l.dz + matrix_bytes(d, M, padded(d, l.piece));
     l.dw = align_up(l.dx + (size_t)(l.more * M * K) * 4, 256);
     l.part = align_up(l.dw + (l.pw.splits > 1 ? (size_t)l.pw.splits * l.piece * K * 4 : 0), 256);
-    l.total = align_up(l.part + (l.small.splits > 1 ? small_bytes(l.small, M, V) : (size_t)((M + 31) / 32 * V) * 4), 256);
+    // the tiles are those of aligned operands or not: what a call has is not known here
+    const Shape s = shape_of(d, M, l.piece, K);
+    const int a = wave_rows((int)M, tiling(s, true)), u = wave_rows((int)M, tiling(s, false));
+    l.total = align_up(l.part + (l.small.splits > 1 ? small_bytes(l.small, M, V) : (size_t)((a > u ? a : u) * V) * 4), 256);
     return l;
 }
 
@@ -570,7 +578,7 @@ void entropy_backward(const void* x, const void* weight, const void* bias, const
         }
     }
     if (gx) join(dx, lay.px.splits, place, {count, dx_tile, lay.more}, M, K, static_cast<T*>(gx), st);
-    if (gb) k_bias_fold<T><<<(V + 63) / 64, kLiveThreads, 0, st>>>(part, count, tiles.bm, tiles.waves_m, V, static_cast<T*>(gb));
+    if (gb) k_bias_fold<T><<<(V + 63) / 64, kLiveThreads, 0, st>>>(part, count, tiles, V, static_cast<T*>(gb));
 }
 
 }  // namespace
