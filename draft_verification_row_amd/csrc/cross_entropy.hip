@@ -124,6 +124,7 @@ template <typename T>
 struct Stats : Logits<T> {
     const int32_t* tokens;
     const int* live;  // or null: every row
+    int v0;           // the product's first column in the vocabulary
     int rows;         // of `part`
     MaxSum* part;
     float* picked;
@@ -142,7 +143,7 @@ struct Stats : Logits<T> {
             all[j] = {top, sum};
 #pragma unroll
             for (int s = C::kB; s < 64; s *= 2) all[j] = joined(all[j], {__shfl_xor(all[j].top, s), __shfl_xor(all[j].sum, s)});
-            const int x = m < p.M ? tokens[live ? live[m] : m] - p.n0 : -1;
+            const int x = m < p.M ? tokens[live ? live[m] : m] - v0 - p.n0 : -1;
             const bool here = x >= 0 && x < C::WN && p.n0 + x < p.N;
             if (__ballot(here) == 0) return;
             lay<C>(p, acc, std::integral_constant<int, j * C::kB / 32>());
@@ -395,6 +396,12 @@ inline Tiling tiling(Shape s, bool direct) {
     if (!direct || s == kLogits64) return {64, 64, 2};
     return s == kRows32 ? Tiling{32, 128, 1} : s == kRows64 ? Tiling{64, 128, 1} : s == kRows192 ? Tiling{192, 128, 2} : s == kLogits256 ? Tiling{256, 256, 2} : Tiling{128, 128, 2};
 }
+// The columns that one launch of such tiles takes: all, or whole tiles of them,
+// so that its threads are counted in 32 bits (64 x 64: M V up to some 2^36).
+inline int launch_columns(int M, int V, const Tiling& t) {
+    const long long most = ((1ll << 32) / kThreads - 1) / ((M + t.bm - 1) / t.bm) * t.bn;
+    return V < most ? V : (int)most;
+}
 template <typename T, class E>
 void launch_logits(const Product& g, const E& e, Shape s, hipStream_t st) {
     if (!aligned(g, sizeof(T)))
@@ -474,8 +481,14 @@ void entropy_forward(const void* x, const void* weight, const void* bias, const 
         return;
     }
     const Shape s = shape_of(d, M, V, K);
-    launch_logits<T>(g, Stats<T>{{static_cast<const T*>(bias)}, tokens, live, M, part, picked}, s, st);
-    const int bn = tiling(s, aligned(g, sizeof(T))).bn;
+    const Tiling t = tiling(s, aligned(g, sizeof(T)));
+    const int bn = t.bn, piece = launch_columns(M, V, t);
+    const T *w = static_cast<const T*>(g.w[0]), *b = static_cast<const T*>(bias);
+    for (int v0 = 0; v0 < V; v0 += piece) {
+        g.N = V - v0 < piece ? V - v0 : piece;
+        g.w[0] = g.w[1] = w + v0 * g.ldw;
+        launch_logits<T>(g, Stats<T>{{b ? b + v0 : nullptr}, tokens, live, v0, M, part + (int64_t)(v0 / bn) * M, picked}, s, st);
+    }
     int across = 1;
     while (across < M && across < 64) across *= 2;
     k_fold<<<(M + across - 1) / across, kLiveThreads, 0, st>>>({part, picked, tokens, live, count, M, V, (V + bn - 1) / bn, across, out});

@@ -142,7 +142,8 @@ static void product(const std::string& n, unsigned grid, void** args) {
         writes("y", o.y, (long long)g.M * g.N * s.e), writes("g", o.g, (long long)g.M * g.N * 4), writes("u", o.u, (long long)g.M * g.N * 4);
     } else if (n.find("Stats<") != std::string::npos) {
         auto& o = *static_cast<const Stats<float>*>(e);
-        stats_tiles = tiles_n;
+        if (o.v0 % columns) fail("a launch inside a tile");
+        stats_tiles = o.v0 / columns + tiles_n;
         reads("tokens", o.tokens, rows_in_all * 4), reads("live", o.live, g.M * 4);
         writes("parts of rows", o.part, ((tiles_n - 1) * o.rows + g.M) * (long long)sizeof(MaxSum)), writes("picked", o.picked, g.M * 4ll);
         reads("bias", o.bias, (long long)g.N * s.e);
@@ -259,7 +260,8 @@ extern "C" {
 hipError_t __hipPushCallConfiguration(dim3 g, dim3 b, size_t, hipStream_t) { return grid_ = g, block_ = b, hipSuccess; }
 hipError_t __hipPopCallConfiguration(dim3* g, dim3* b, size_t* shared, hipStream_t* st) { return *g = grid_, *b = block_, *shared = 0, *st = nullptr, hipSuccess; }
 hipError_t hipLaunchKernel(const void* f, dim3 g, dim3 b, void** args, size_t, hipStream_t) {
-    if (g.y != 1 || g.z != 1 || b.y != 1 || b.z != 1 || g.x < 1) fail("grid of " + std::to_string(g.x));
+    // the hardware counts a launch's threads in 32 bits
+    if (g.y != 1 || g.z != 1 || b.y != 1 || b.z != 1 || g.x < 1 || (uint64_t)g.x * b.x >> 32) fail("grid of " + std::to_string(g.x) + ", " + names[f]);
     launch(names[f], g.x, b.x, args);
     return hipSuccess;
 }
@@ -359,6 +361,16 @@ int main() {
         gated_calls(dt, 8192, 14336, 4096, 0), gated_calls(dt, 8191, 14337, 4095, 0), gated_calls(dt, 100000, 24, 16, 0), gated_calls(dt, 70, 90, 50001, 0);
         embedding_calls(dt, 1 << 20, 128256, 4096, 0), embedding_calls(dt, 32768, 1 << 20, 8191, 0), embedding_calls(dt, 1, 1, 1 << 20, 0);
     }
+    // the largest that are taken: 2^20 a size, and what the products allow
+    const int most = 1 << 20;
+    for (spec_dtype dt : {SPEC_BF16, SPEC_F32})
+        for (int off : {0, (int)elem(dt)})
+            for (int a : {1, 17, 65, 8191, 65535, 262144, most})
+                for (int b : {1, 31, 4097, 65536, 262143, most})
+                    for (int c : {1, 3, 64, 1023, 8189, 65535, most}) {
+                        if (spec_embedding_grad_workspace_bytes(dt, a, b, c)) embedding_calls(dt, a, b, c, off);
+                        if (spec_cross_entropy_workspace_bytes(dt, a, b, c)) entropy_calls(dt, a, b, c, off, true);
+                    }
     printf("%ld launches, %d failures\n", launches, failures);
     return failures != 0;
 }

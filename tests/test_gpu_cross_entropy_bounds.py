@@ -6,7 +6,7 @@ import torch
 
 import draft_verification_row_amd as sv
 from test_gpu_cross_entropy import check, make
-from test_gpu_embedding import DT, at_offset
+from test_gpu_embedding import DT, U, at_offset, close
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,31 @@ def test_gradients_stay_in_their_workspace(M, V, K, dtype, off):
 @pytest.mark.parametrize("M,V,K", CASES)
 def test_gradients_with_every_row_in_use(M, V, K, dtype, off):
     check(M, V, K, dtype, bias=True, pad=0.0, off=off)
+
+
+def test_more_tiles_than_a_launch_counts():
+    """2^24 tiles of 64 x 64, whose threads pass 32 bits: they go in two launches.
+    Four different rows of x, so that the float64 form is small.  Tolerances as in
+    test_gpu_cross_entropy: a row's 4096 parts are joined 256 to a thread, after
+    18 values in a lane and before 4 more steps."""
+    M = V = 1 << 18
+    K, last = 8, (1 << 18) - 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = at_offset((torch.randn(V, K, generator=g, device="cuda") / 2).bfloat16(), 1)
+    b = (torch.randn(V, generator=g, device="cuda") / 2).bfloat16()
+    rows = torch.randn(4, K, generator=g, device="cuda").bfloat16()
+    x = rows.repeat(M // 4, 1)
+    tok = torch.randint(-1, V, (M,), generator=g, device="cuda", dtype=torch.int32)
+    tok[:128] = torch.arange(last - 64, V, dtype=torch.int32, device="cuda")  # on either side
+    out = sv.spec_cross_entropy(x, w, tok, b)
+    rd, wd, bd = rows.double(), w.double(), b.double()
+    z = rd @ wd.t() + bd
+    e = (2 * U * (K + 9) * (rd.abs() @ wd.abs().t() + bd.abs())).amax(1).repeat(M // 4)
+    n = torch.logsumexp(z, 1)
+    on = tok >= 0
+    loss = n.repeat(M // 4) - z[torch.arange(M, device="cuda") % 4, tok.long().clamp_min(0)]
+    lse = n.repeat(M // 4)
+    size = U * (600 + 4 * lse.abs() + 4 * loss.abs())
+    close(out.lse[on], lse[on], (e + size)[on], "lse")
+    close(out.loss[on], loss[on], (2 * e + size)[on], "loss")
+    assert (out.loss[~on] == 0).all() and (out.lse[~on] == 0).all() and (out.status == 0).all()
