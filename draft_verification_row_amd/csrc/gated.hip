@@ -223,10 +223,10 @@ struct Pads {
     int64_t end[3];  // rows up to the end of each
 };
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_pad_rows(Pads a, int K, int64_t ld) {
+__global__ __launch_bounds__(kThreads) void k_pad_rows(Pads a, int K, int64_t ld, int64_t first) {
     constexpr int kElems = 16 / (int)sizeof(T);
     const int64_t across = ld / kElems, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    int64_t m = i / across;
+    int64_t m = first + i / across;
     if (m >= a.end[2]) return;
     const int which = m >= a.end[1] ? 2 : m >= a.end[0], k = (int)(i % across) * kElems;
     if (which) m -= a.end[which - 1];
@@ -246,8 +246,12 @@ Padded pad_rows(const void* x, const void* gate, const void* up, spec_dtype d, i
     a.end[0] = x ? M : 0;
     a.end[1] = a.end[0] + (gate ? N : 0);
     a.end[2] = a.end[1] + (up ? N : 0);
-    const int64_t n = a.end[2] * (ld / (16 / (int64_t)sizeof(T)));
-    if (n) k_pad_rows<T><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(a, K, ld);
+    // one launch, but its threads are counted in 32 bits
+    const int64_t across = ld / (16 / (int64_t)sizeof(T)), most = ((1ll << 32) - kThreads) / across;
+    for (int64_t m = 0; m < a.end[2]; m += most) {
+        const int64_t rows = a.end[2] - m < most ? a.end[2] - m : most;
+        k_pad_rows<T><<<(unsigned)((rows * across + kThreads - 1) / kThreads), kThreads, 0, st>>>(a, K, ld, m);
+    }
     return {px, pg, pu, ld};
 }
 

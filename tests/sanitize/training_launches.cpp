@@ -71,11 +71,14 @@ static void reads(const char* what, const void* p, long long bytes, long long sl
         if (r.second.first <= a && a + bytes <= r.second.second) return;
     fail(std::string(what) + " is read where nothing was written");
 }
+static long long pad_rows_done, pad_rows_asked;
 static void finish(spec_status s) {
     if (s != SPEC_OK) fail("returned " + std::to_string((int)s));
     for (auto a = parts.begin(); a != parts.end(); ++a)
         for (auto b = std::next(a); b != parts.end(); ++b)
             if (a->second.first < b->second.second && b->second.first < a->second.second) fail(a->first + " overlaps " + b->first);
+    if (pad_rows_done < pad_rows_asked) fail("rows left out of the padding");
+    pad_rows_done = pad_rows_asked = 0;
     parts.clear();
 }
 
@@ -211,7 +214,11 @@ static void launch(const std::string& n, unsigned grid, unsigned block, void** a
             const long long rows = a.end[i] - (i ? a.end[i - 1] : 0);
             if (rows) reads(what[i], a.from[i], rows * K * e), writes(what[i], a.to[i], rows * ld * e);
         }
-        if ((long long)grid * block < a.end[2] * (ld / (16 / e))) fail("grid below its rows");
+        // launches of some of the rows each
+        const long long first = arg<int64_t>(args, 3);
+        if (first > pad_rows_done) fail("rows left out of the padding");
+        pad_rows_done = first + (long long)grid * block / (ld / (16 / e));
+        pad_rows_asked = a.end[2];
     } else if (is("k_join")) {
         const Live& live = arg<Live>(args, 4);
         const long long s = live.count && live.more > arg<int>(args, 1) ? live.more : arg<int>(args, 1), M = arg<int>(args, 5), N = arg<int>(args, 6);
@@ -369,6 +376,7 @@ int main() {
                 for (int b : {1, 31, 4097, 65536, 262143, most})
                     for (int c : {1, 3, 64, 1023, 8189, 65535, most}) {
                         if (spec_embedding_grad_workspace_bytes(dt, a, b, c)) embedding_calls(dt, a, b, c, off);
+                        if (spec_gated_linear_workspace_bytes(dt, a, b, c)) gated_calls(dt, a, b, c, off);
                         if (spec_cross_entropy_workspace_bytes(dt, a, b, c)) entropy_calls(dt, a, b, c, off, true);
                     }
     printf("%ld launches, %d failures\n", launches, failures);

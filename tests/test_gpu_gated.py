@@ -222,3 +222,20 @@ def test_gated_past_32_bits_of_offset():
         x = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
         y = sv.spec_gated_linear(x, w, w, activation="relu").float()
         assert (y[:, -1] == torch.tensor(float(K) ** 2).bfloat16().item()).all() and y.count_nonzero() == 2 * M
+
+
+def test_gated_more_padding_than_a_launch_counts():
+    """Rows of odd length that are padded by more than 2^32 threads: two launches."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("needs 103 GB of free memory")
+    M, N, K = 17, 16384, 524285
+    x = torch.ones(M, K, device="cuda")
+    w = torch.zeros(N, K, device="cuda")
+    w[-1], w[-10], w[5] = 1.0, 2.0, 3.0  # the second launch has the last rows of the second matrix
+    y = sv.spec_gated_linear(x, w, w, activation="relu")
+    for n, v in ((-1, 1), (-10, 2), (5, 3)):
+        assert (y[:, n] == torch.tensor(float(v * K) ** 2, device="cuda").float()).all(), n
+    assert y.count_nonzero() == 3 * M
+    del x, w, y
+    torch.cuda.empty_cache()
