@@ -386,7 +386,7 @@ enum Shape { kRows32, kRows64, kRows192, kLogits256, kLogits128, kLogits64 };
 inline Shape shape_of(spec_dtype d, long long M, long long V, long long K) {
     if (M <= 32) return kRows32;
     if (M <= 64) return kRows64;
-    const Size s = plan_of(d, M, V, K, 1, false, true).size;
+    const Size s = plan_of(d, M, V, K, 1, kNoSums, true).size;
     return s == kTile192 ? kRows192 : s == kTile256 ? kLogits256 : s == kTile128 ? kLogits128 : kLogits64;
 }
 // Where W's rows are no whole chunks, they are copied to padded ones first if
@@ -423,8 +423,12 @@ void pack(const void* x, const int* live, const int* count, long long rows, int 
 }
 inline size_t matrix_bytes(spec_dtype d, long long rows, long long ld) { return align_up((size_t)(rows * ld) * elem(d), 256); }
 
-// Few tiles of a long sum: it is split.
-inline Plan small_plan(spec_dtype d, long long M, long long V, long long K) { return plan_of(d, M, V, K, 1, true, false); }
+// Few tiles of a long sum: it is split, as far as the logits of all splits stay
+// within kSumsBytes.  By time alone they would take 8.4 GB of 16384 x 32000 x 65536
+// fp32 (four splits).  Half of it costs 36838 x 2615 x 52288 bf16 its two splits:
+// 9.9 -> 11.4 ms.
+constexpr long long kSumsBytes = 1ll << 30;
+inline Plan small_plan(spec_dtype d, long long M, long long V, long long K) { return plan_of(d, M, V, K, 1, kSumsBytes, false); }
 inline size_t small_bytes(const Plan& p, long long M, long long V) { return p.splits > 1 ? align_up((size_t)(p.splits * M * V) * 4, 256) : 0; }
 
 struct ForwardLayout {
@@ -512,8 +516,8 @@ inline BackwardLayout backward_layout(spec_dtype d, long long M, long long V, lo
     l.small = small_plan(d, M, V, K);
     if (l.small.splits > 1) l.piece = (int)V;
     l.packs = packs_weight(d, M, K);
-    l.px = plan_of(d, M, K, l.piece, 1, true, false);
-    l.pw = plan_of(d, l.piece, K, M, 1, true, false);
+    l.px = plan_of(d, M, K, l.piece, 1, kAnySums, false);
+    l.pw = plan_of(d, l.piece, K, M, 1, kAnySums, false);
     // room for up to four times the compute units' tiles
     const long long b = 256 >> l.px.size, tiles = ((M + b - 1) / b) * ((K + b - 1) / b), most = 1024 / tiles;
     l.more = (int)(most > kMaxSplits ? kMaxSplits : most < l.px.splits ? l.px.splits : most);

@@ -255,7 +255,7 @@ Padded pad_rows(const void* x, const void* gate, const void* up, spec_dtype d, i
     return {px, pg, pu, ld};
 }
 
-inline Plan gated_plan(spec_dtype d, long long M, long long N, long long K) { return plan_of(d, M, 2 * N, K, 1, true, true); }
+inline Plan gated_plan(spec_dtype d, long long M, long long N, long long K) { return plan_of(d, M, 2 * N, K, 1, kAnySums, true); }
 inline size_t gated_packs(spec_dtype d, long long M, long long N, long long K) {
     return packs_pair(d, M, K) ? packed_bytes(d, M, K) + 2 * packed_bytes(d, N, K) : 0;
 }
@@ -318,8 +318,8 @@ inline GatedLayout gated_layout(spec_dtype d, long long M, long long N, long lon
     l.du = align_up((size_t)(M * l.np) * elem(d), 256);
     l.packed = 2 * l.du;
     l.sums = l.packed + (packs_pair(d, M, K) ? packed_bytes(d, M, K) + 2 * packed_bytes(d, N, K) : 0);
-    l.x = plan_of(d, M, K, 2 * N, 1, true, false);
-    l.w = plan_of(d, N, K, M, 2, true, false);
+    l.x = plan_of(d, M, K, 2 * N, 1, kAnySums, false);
+    l.w = plan_of(d, N, K, M, 2, kAnySums, false);
     const size_t a = l.x.splits > 1 ? (size_t)(l.x.splits * M * K) * 4 : 0, b = l.w.splits > 1 ? (size_t)(2 * l.w.splits * N * K) * 4 : 0;
     l.total = l.sums + align_up(a > b ? a : b, 256);
     return l;

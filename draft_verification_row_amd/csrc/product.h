@@ -697,13 +697,14 @@ inline unsigned four_blocks(long long M, long long N) { return (unsigned)((M * (
 // once for; only where `tall` (192 x 14336 x 4096, a pair: 49 us, 65 with tiles of
 // 64).
 constexpr int kMaxSplits = 32;
+constexpr long long kNoSums = 0, kAnySums = 1ll << 62;  // `room`: bytes that the splits' sums may take
 enum Size { kTile256, kTile128, kTile64, kTile192 };
 struct Plan {
     Size size;
     int splits;
 };
 inline long long step_of(spec_dtype d) { return 128 / (long long)elem(d); }
-inline Plan plan_of(spec_dtype d, long long M, long long N, long long K, int products, bool splitting, bool tall) {
+inline Plan plan_of(spec_dtype d, long long M, long long N, long long K, int products, long long room, bool tall) {
     static const double kStepTime[2][4] = {{7.2, 1.85, 0.95, 2.8}, {1.4, 0.6, 0.5, 0.5}}, kBeside[4] = {12, 7, 5, 7};
     static const int kRows[4] = {256, 128, 64, 192}, kColumns[4] = {256, 128, 64, 128};
     const long long steps = (K + step_of(d) - 1) / step_of(d);
@@ -712,7 +713,7 @@ inline Plan plan_of(spec_dtype d, long long M, long long N, long long K, int pro
     for (int z = 0; z < (tall ? 4 : 3); ++z) {
         const long long slots = z == kTile64 ? 512 : 256;
         const long long tiles = ((M + kRows[z] - 1) / kRows[z]) * ((N + kColumns[z] - 1) / kColumns[z]) * products;
-        for (int s = 1; s <= (splitting ? kMaxSplits : 1) && s <= steps; ++s) {
+        for (int s = 1; s <= kMaxSplits && s <= steps && (s == 1 || s * M * N * products * 4 <= room); ++s) {
             const long long per = (steps + s - 1) / s, rounds = (tiles * s + slots - 1) / slots;
             double us = rounds * (per * kStepTime[d == SPEC_BF16][z] + kBeside[z]);
             if (s > 1) us += 4 + (double)(s * M * N * products) * 8 / 4e6;

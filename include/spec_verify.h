@@ -659,8 +659,8 @@ spec_status spec_gated_linear_grad(const void *x, const void *gate, const void *
 /*
  * The cross entropy of given tokens under a head's output layer, whose logits z
  * = x W^T + bias are not kept (products of few tiles, whose sums over K are
- * split, have up to some 130 MB of them in the workspace): out_loss[m] = -log softmax(z_m)[tokens[m]]
- * and out_lse[m] = log sum e^(z_m), in nats, from fp32 products and sums.
+ * split, have up to 1 GiB of them in the workspace, all splits together):
+ * out_loss[m] = -log softmax(z_m)[tokens[m]] and out_lse[m] = log sum e^(z_m), in nats, from fp32 products and sums.
  * tokens[m] = -1 marks a padded row, which does not enter any result: its loss
  * and lse are 0, and its row of x is not used.  A bias of -inf takes a token
  * out of the vocabulary: its probability is 0, a row with that token has a

@@ -72,6 +72,7 @@ static void reads(const char* what, const void* p, long long bytes, long long sl
     fail(std::string(what) + " is read where nothing was written");
 }
 static long long pad_rows_done, pad_rows_asked;
+static size_t most_dz = ~(size_t)0;  // its bytes in this call
 static void finish(spec_status s) {
     if (s != SPEC_OK) fail("returned " + std::to_string((int)s));
     for (auto a = parts.begin(); a != parts.end(); ++a)
@@ -79,6 +80,9 @@ static void finish(spec_status s) {
             if (a->second.first < b->second.second && b->second.first < a->second.second) fail(a->first + " overlaps " + b->first);
     if (pad_rows_done < pad_rows_asked) fail("rows left out of the padding");
     pad_rows_done = pad_rows_asked = 0;
+    // what the header says of the cross entropy's workspace
+    for (auto& p : parts)
+        if ((p.first == "dz" && p.second.second - p.second.first > most_dz) || (p.first == "logits" && p.second.second - p.second.first > 1u << 30)) fail(p.first + " take " + std::to_string(p.second.second - p.second.first) + " bytes");
     parts.clear();
 }
 
@@ -290,6 +294,7 @@ static std::string title(const char* op, spec_dtype dt, long long a, long long b
 }
 static void embedding_calls(spec_dtype dt, int n, int V, int H, int off) {
     const size_t e = elem(dt);
+    most_dz = ~(size_t)0;
     begin(title("embedding", dt, n, V, H, off));
     auto* w = buffer<void>("weight", (size_t)V * H * e, off);
     auto* tok = buffer<int32_t>("tokens", n * 4ull);
@@ -300,6 +305,7 @@ static void embedding_calls(spec_dtype dt, int n, int V, int H, int off) {
     finish(spec_embedding_grad(tok, gy, dt, 1.f, n, V, H, gw, buffer<void>("workspace", need), need, nullptr));
 }
 static void gated_calls(spec_dtype dt, int M, int N, int K, int off, bool forward_only = false) {
+    most_dz = ~(size_t)0;
     const size_t e = elem(dt), x_ = (size_t)M * K * e, w_ = (size_t)N * K * e, y_ = (size_t)M * N * e, f_ = (size_t)M * N * 4;
     for (int keep = 0; keep < 2; ++keep) {
         begin(title("gated", dt, M, N, K, off));
@@ -328,6 +334,7 @@ static void entropy_calls(spec_dtype dt, int M, int V, int K, int off, bool all_
     const size_t e = elem(dt), x_ = (size_t)M * K * e, w_ = (size_t)V * K * e;
     begin(title("cross entropy", dt, M, V, K, off));
     rows_in_all = M;
+    most_dz = M * 1024ull * e > 512 << 20 ? M * 1024ull * e : 512 << 20;
     auto *x = buffer<void>("x", x_, all_off ? off : 0), *w = buffer<void>("weight", w_, off), *b = buffer<void>("bias", V * e, all_off ? off : 0);
     auto* tok = buffer<int32_t>("tokens", M * 4ull);
     auto* stats = buffer<float>("stats", M * 8ull);
@@ -368,6 +375,11 @@ int main() {
         gated_calls(dt, 8192, 14336, 4096, 0), gated_calls(dt, 8191, 14337, 4095, 0), gated_calls(dt, 100000, 24, 16, 0), gated_calls(dt, 70, 90, 50001, 0);
         embedding_calls(dt, 1 << 20, 128256, 4096, 0), embedding_calls(dt, 32768, 1 << 20, 8191, 0), embedding_calls(dt, 1, 1, 1 << 20, 0);
     }
+    // long sums of many logits, which are split
+    for (spec_dtype dt : {SPEC_BF16, SPEC_F32})
+        for (int M : {50, 203, 1061, 5111, 8475, 20654, 36838})
+            for (int V : {379, 2615, 4452, 14023, 81876})
+                for (int K : {4096, 8192, 16384, 52288, 65536}) entropy_calls(dt, M, V, K, 0, false);
     // the largest that are taken: 2^20 a size, and what the products allow
     const int most = 1 << 20;
     for (spec_dtype dt : {SPEC_BF16, SPEC_F32})
