@@ -2,11 +2,12 @@
 // table's gradient, for gfx950 (MI355X).
 //
 //   y[i] = s W[t_i]                     W [V][H], y [n][H]
-//   dW[v] = s sum over i with t_i = v of dy[i], in the order of i
+//   dW[v] = s sum over i with t_i = v of dy[i]
 // Both are bound by memory.  The gradient is made row by row of the table, with
 // the positions sorted by token, so that each of its bytes is written once, no
-// two workgroups add to the same one, and the order of its sums is fixed.  Sums
-// are fp32 and rounded once.
+// two workgroups add to the same one, and the order of its sums is fixed (that of i,
+// with each whole piece of a long run summed by itself).  Sums are fp32 and
+// rounded once.
 #include "tiles.h"
 
 namespace {

@@ -693,11 +693,11 @@ inline unsigned four_blocks(long long M, long long N) { return (unsigned)((M * (
 // by a plain count, of rounds of workgroups, steps in each, and the bytes of the
 // splits' sums.  Microseconds: a tile's step (128 bytes of k; two tiles of 64 share
 // a compute unit), and what a workgroup takes beside its steps.  kTile192 is 192
-// rows by 128 columns, for products of up to that many rows, which it reads W
-// once for; only where `tall` (192 x 14336 x 4096, a pair: 49 us, 65 with tiles of
-// 64).
+// rows by 128 columns, only where `tall`: products of up to that many rows read W
+// once (192 x 14336 x 4096, a pair: 49 us, 65 with tiles of 64); the count takes it
+// for others as well.  `room`: the bytes that the splits' sums may take.
 constexpr int kMaxSplits = 32;
-constexpr long long kNoSums = 0, kAnySums = 1ll << 62;  // `room`: bytes that the splits' sums may take
+constexpr long long kNoSums = 0, kAnySums = 1ll << 62;
 enum Size { kTile256, kTile128, kTile64, kTile192 };
 struct Plan {
     Size size;

@@ -75,7 +75,7 @@ def spec_embedding(weight: torch.Tensor, tokens: torch.Tensor, *, scale: float =
     weight [V][H] bfloat16 or float32; tokens int32.  A token of -1 pads its
     position, as in the rules' outputs, and gives zeros; any other outside
     [0, V) gives NaN.  The weight has a gradient, a whole table: each token's
-    positions are summed in float32, in their order.
+    positions are summed in float32, in a fixed order.
     """
     W = _check(weight, "weight")
     if W.dim() != 2 or W.numel() == 0:
